@@ -18,3 +18,7 @@ from .layer import (  # noqa: F401
     device_check, selftest_wait_timeout, make_problem, torch_distributed_allreduce, swa_fwd,
     swa_workspace_bytes,
 )
+from .attention import (  # noqa: F401
+    rotary_fwd, rotary_bwd, rotary_frequencies, swa_sink_fwd, swa_sink_bwd, swa_sink_bwd_workspace_bytes,
+    swa_sink_decode, swa_cache_fill,
+)

@@ -55,6 +55,22 @@ class LactSwaProblem(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class LactTensor4(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64)]
+
+
+class LactRotaryProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "H", "Hkv", "T", "d", "rot", "start")] + [
+        ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32), ("amplitude", ctypes.c_float),
+        ("reserved", ctypes.c_int32)]
+
+
+class LactSwaSinkProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "H", "Hkv", "T", "Tq", "d", "window", "sinks")] + [
+        ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
 class LactError(RuntimeError):
     def __init__(self, code: int, what: str = ""):
         self.code = code
@@ -63,6 +79,9 @@ class LactError(RuntimeError):
 
 _P = ctypes.POINTER(LactProblem)
 _vp = ctypes.c_void_p
+_RP = ctypes.POINTER(LactRotaryProblem)
+_SP = ctypes.POINTER(LactSwaSinkProblem)
+_T4 = ctypes.POINTER(LactTensor4)
 # name -> (restype, argtypes); the exported surface of include/lact.h
 SIGNATURES = {
     "lact_ttt_workspace_bytes": (ctypes.c_size_t, [_P]),
@@ -79,6 +98,16 @@ SIGNATURES = {
     "lact_ttt_fwd_host": (ctypes.c_int, [_P] + [_vp] * 12 + [_vp, ctypes.c_size_t, _vp]),
     "lact_swa_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(LactSwaProblem)]),
     "lact_swa_fwd": (ctypes.c_int, [ctypes.POINTER(LactSwaProblem)] + [_vp] * 8 + [_vp, ctypes.c_size_t, _vp]),
+    "lact_rotary_fwd": (ctypes.c_int, [_RP, _T4, _T4] + [_vp] * 6 + [_T4, _T4, _vp]),
+    "lact_rotary_bwd_workspace_bytes": (ctypes.c_size_t, [_RP]),
+    "lact_rotary_bwd": (ctypes.c_int, [_RP, _T4, _T4, _vp, _vp, _T4, _T4, _vp, _vp, _T4, _T4] + [_vp] * 5
+                        + [ctypes.c_size_t, _vp]),
+    "lact_swa_sink_fwd": (ctypes.c_int, [_SP, _T4, _T4, _T4, _vp, _T4, _vp, _vp]),
+    "lact_swa_sink_bwd_workspace_bytes": (ctypes.c_size_t, [_SP]),
+    "lact_swa_sink_bwd": (ctypes.c_int, [_SP, _T4, _T4, _T4, _T4, _vp, _T4, _vp, _T4, _T4, _T4, _vp,
+                                         ctypes.c_size_t, _vp]),
+    "lact_swa_sink_decode": (ctypes.c_int, [_SP, _T4, _T4, _T4, _vp, _vp, _vp, _T4, _vp]),
+    "lact_swa_cache_fill": (ctypes.c_int, [_SP, _T4, _T4, _vp, _vp, _vp, _vp]),
     "lact_ttt_status": (ctypes.c_int, [_vp]),
     "lact_device_check": (ctypes.c_int, []),
     "lact_ttt_launch_count": (ctypes.c_int64, [_P]),

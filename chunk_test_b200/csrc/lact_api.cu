@@ -15,6 +15,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <utility>
@@ -402,14 +403,16 @@ static cudaError_t launch_gemm_any(bool split, int bn, dim3 grid, const GemmPara
 enum Kind {
   K_INIT, K_PROLOGUE, K_BETA_MEAN, K_FWD_QUERY, K_APPLY_OUT, K_FWD_KEY, K_GRAD, K_NS_SUMSQ,
   K_NS_SCALE, K_NS_GRAM, K_NS_POLY, K_NS_UPDATE, K_RULE, K_FINALIZE, K_SIMT_GEMM, K_FWD_ELEM_F32,
-  K_APPLY_FUSED, K_KEY_GRAD, K_BWD_ELEM, K_BWD_GEMM, K_SWA, K_SWA_GEMM, K_SWA_FLASH, K_BWD_KEY, K_BWD_APPLY, K_COUNT
+  K_APPLY_FUSED, K_KEY_GRAD, K_BWD_ELEM, K_BWD_GEMM, K_SWA, K_SWA_GEMM, K_SWA_FLASH, K_BWD_KEY, K_BWD_APPLY,
+  K_ROTARY, K_ROTARY_SUMS, K_WATTN_FWD, K_WATTN_DQ, K_WATTN_DKV, K_WATTN_ELEM, K_WATTN_DECODE, K_COUNT
 };
 static const char* const kKindNames[K_COUNT] = {
     "init_state", "qk_prologue", "beta_mean", "fwd_query_umma", "apply_out_umma", "fwd_key_umma",
     "grad_umma", "ns_sumsq", "ns_scale", "ns_gram_umma", "ns_poly_umma", "ns_update_umma",
     "rule_renorm", "finalize_state", "simt_gemm_f32", "fwd_elem_f32", "apply_fused_umma",
     "key_grad_umma", "bwd_elem", "bwd_gemm_umma", "swa_elem", "swa_gemm_umma", "swa_flash_umma",
-    "bwd_key_umma", "bwd_apply_umma"};
+    "bwd_key_umma", "bwd_apply_umma", "rotary", "rotary_sums", "wattn_fwd", "wattn_dq", "wattn_dkv", "wattn_elem",
+    "wattn_decode"};
 
 // Optional per-launch CUDA-event pairs on the launching stream.
 struct ProfRec { int kind; cudaEvent_t a, b; };
@@ -1109,6 +1112,7 @@ __global__ void k_selftest_wait(long long budget) {
 
 #include "lact_bwd.cuh"
 #include "lact_swa.cuh"
+#include "lact_wattn.cuh"
 
 using namespace lact;
 

@@ -1,0 +1,575 @@
+// lact_wattn.cuh -- host side of the attention half's operators: rotary
+// positions, the window attention with sinks (forward, backward) and its
+// single-token form over a rolling cache.  Included by lact_api.cu after the
+// launch helpers.
+#pragma once
+
+#include "wattn_decode.cuh"
+#include "wattn_simt.cuh"
+
+namespace lact {
+
+// ------------------------------------------------------------------ arguments
+struct Extent4 {
+  int64_t B, H, T, d;
+};
+
+static bool view_ok(const lact_tensor4* t, const Extent4& e, int esz) {
+  if (!t || !t->data || !aligned16(t->data)) return false;
+  const int64_t s[3] = {t->stride_b, t->stride_h, t->stride_t}, n[3] = {e.B, e.H, e.T};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (s[i] <= 0 || s[i] * esz % 16 != 0 || s[i] > (int64_t(1) << 36))) return false;
+  return true;
+}
+
+// Strides of dimensions of length 1 mean nothing to the caller; they are set
+// to the ones a dense tensor would have.
+static View4 view4(const lact_tensor4* t, const Extent4& e) {
+  View4 v{t->data, t->stride_b, t->stride_h, t->stride_t};
+  if (e.T == 1) v.st = e.d;
+  if (e.H == 1) v.sh = e.T > 1 ? v.st * e.T : e.d;
+  if (e.B == 1) v.sb = std::max(v.sh * e.H, v.st * e.T);
+  return v;
+}
+
+static int64_t span(const View4& v, const Extent4& e) {   // elements from the first to behind the last
+  return (e.B - 1) * v.sb + (e.H - 1) * v.sh + (e.T - 1) * v.st + e.d;
+}
+
+// No two elements of the view share an address: by ascending stride, each
+// dimension steps over all of the ones below it.
+static bool injective(const View4& v, const Extent4& e) {
+  std::pair<int64_t, int64_t> s[3] = {{v.sb, e.B}, {v.sh, e.H}, {v.st, e.T}};
+  std::sort(s, s + 3);
+  int64_t reach = e.d;
+  for (auto& x : s) {
+    if (x.second == 1) continue;
+    if (x.first < reach) return false;
+    reach = x.first * (x.second - 1) + reach;
+  }
+  return true;
+}
+
+// Whether two views share no memory: their spans are apart, or both are slices
+// of one packed [B, T, row] buffer (equal row pitch) in different columns.
+static bool apart(const View4& a, const Extent4& ea, const View4& b, const Extent4& eb, int esz) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  if (!overlaps(a.p, static_cast<size_t>(span(a, ea)) * esz, b.p, static_cast<size_t>(span(b, eb)) * esz)) return true;
+  if (a.st != b.st || ea.T < 2 || eb.T < 2) return false;
+  if ((ea.B > 1 && a.sb % a.st != 0) || (eb.B > 1 && b.sb % b.st != 0)) return false;
+  const int64_t wa = (ea.H - 1) * a.sh + ea.d, wb = (eb.H - 1) * b.sh + eb.d;
+  const int64_t pitch = a.st * esz;
+  const int64_t at = static_cast<int64_t>(((static_cast<int64_t>(pb - pa)) % pitch + pitch) % pitch);
+  return at >= wa * esz && at + wb * esz <= pitch;
+}
+static bool same(const View4& a, const View4& b, const Extent4& e) {
+  return a.p == b.p && (e.B == 1 || a.sb == b.sb) && (e.H == 1 || a.sh == b.sh) && (e.T == 1 || a.st == b.st);
+}
+static bool apart_from(const View4& a, const Extent4& e, int esz, const void* p, int64_t bytes) {
+  return !p || !overlaps(a.p, static_cast<size_t>(span(a, e)) * esz, p, static_cast<size_t>(bytes));
+}
+
+// Raises a kernel's dynamic shared memory limit, once per device.
+template <class F>
+static cudaError_t set_smem(F* kernel, int bytes, bool (&done)[64], bool big_cluster = false) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && big_cluster) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
+}
+
+// ------------------------------------------------------------------ rotary
+struct RotaryDims {
+  int64_t tiles;
+  int tile, pairs, vec, heads_per_block, smem;
+};
+
+static int rotary_validate(const lact_rotary_problem* p) {
+  if (!p || p->B < 1 || p->H < 1 || p->Hkv < 0 || p->T < 1 || p->d < 1) return LACT_EINVAL;
+  if (p->dtype != LACT_F32 && p->dtype != LACT_BF16) return LACT_EINVAL;
+  if (p->d % 8 != 0 || p->d > 512 || p->rot < 2 || p->rot > p->d || p->rot % 2 != 0) return LACT_EINVAL;
+  if (p->B * (p->H + p->Hkv) > 65535 || p->T > (int64_t(1) << 30) || p->B > 65535) return LACT_EINVAL;
+  if (p->start < 0 || p->start > (int64_t(1) << 40) || (p->interleaved & ~1)) return LACT_EINVAL;
+  if (!(std::isfinite(p->amplitude))) return LACT_EINVAL;
+  return LACT_OK;
+}
+
+// Vectors of 16 bytes where both halves of a pair start on one; tiles of 64
+// tokens (less where their angles would pass 64 KB or the tokens would not
+// fill the machine); the heads are split over blocks while there are fewer
+// than two blocks per SM, so that a single token's heads run at once.
+static RotaryDims rotary_dims(const lact_rotary_problem* p, bool sums) {
+  RotaryDims r;
+  const int full = p->dtype == LACT_BF16 ? 8 : 4;
+  r.vec = p->interleaved || (p->rot / 2) % full == 0 ? full : 1;
+  const int step = p->interleaved ? full / 2 : r.vec;
+  r.pairs = static_cast<int>(rup(p->rot / 2, step));
+  const int64_t want = 2 * kPlanSMs;
+  int64_t tile = std::min<int64_t>(64, std::max<int64_t>(1, 8192 / r.pairs));
+  tile = std::min(tile, p->T);
+  while (tile > 16 && p->B * cdiv(p->T, tile) < want) tile /= 2;
+  r.tile = static_cast<int>(tile);
+  r.tiles = p->B * cdiv(p->T, tile);
+  const int64_t heads = p->H + p->Hkv;
+  const int64_t groups = std::min(heads, std::max<int64_t>(1, cdiv(want, r.tiles)));
+  r.heads_per_block = static_cast<int>(cdiv(heads, groups));
+  const int threads = r.vec == 1 ? 512 : 256;
+  const int rot_units = p->interleaved ? 0 : static_cast<int>(p->rot / (2 * r.vec));
+  const int units = p->interleaved ? static_cast<int>(p->d) / r.vec
+                                   : rot_units + static_cast<int>(p->d - p->rot) / r.vec;
+  r.smem = r.tile * r.pairs * 8 + (sums ? threads / units * static_cast<int>(p->d) * 4 : 0);
+  return r;
+}
+
+static size_t rotary_bwd_workspace(const lact_rotary_problem* p) {
+  const RotaryDims r = rotary_dims(p, true);
+  return static_cast<size_t>(rup(r.tiles * 2 * (p->H + p->Hkv) * p->d * 4, 256));
+}
+
+template <typename T, int V, bool INTER, bool BWD, bool AFF>
+static cudaError_t launch_rotary(const RotaryDims& r, const RotaryParams& a, cudaStream_t st) {
+  static bool done[64] = {};
+  const cudaError_t e = set_smem(k_rotary<T, V, INTER, BWD, AFF>, 160 * 1024, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(r.tiles), static_cast<unsigned>(cdiv(a.H + a.Hkv, r.heads_per_block)));
+  return launch_pdl(k_rotary<T, V, INTER, BWD, AFF>, grid, dim3(kRotaryThreads<V>), r.smem, st, a);
+}
+
+template <bool BWD, bool AFF>
+static cudaError_t launch_rotary_any(const lact_rotary_problem* p, const RotaryDims& r, const RotaryParams& a,
+                                     cudaStream_t st) {
+  using B16 = __nv_bfloat16;
+  if (p->dtype == LACT_BF16) {
+    if (p->interleaved) return launch_rotary<B16, 8, true, BWD, AFF>(r, a, st);
+    return r.vec == 8 ? launch_rotary<B16, 8, false, BWD, AFF>(r, a, st)
+                      : launch_rotary<B16, 1, false, BWD, AFF>(r, a, st);
+  }
+  if (p->interleaved) return launch_rotary<float, 4, true, BWD, AFF>(r, a, st);
+  return r.vec == 4 ? launch_rotary<float, 4, false, BWD, AFF>(r, a, st)
+                    : launch_rotary<float, 1, false, BWD, AFF>(r, a, st);
+}
+
+static RotaryParams rotary_params(const lact_rotary_problem* p, const RotaryDims& r, const double* freqs,
+                                  const int32_t* positions) {
+  RotaryParams a;
+  std::memset(&a, 0, sizeof(a));
+  a.freqs = freqs; a.positions = positions; a.start = p->start; a.T = p->T;
+  a.B = static_cast<int>(p->B); a.H = static_cast<int>(p->H); a.Hkv = static_cast<int>(p->Hkv);
+  a.d = static_cast<int>(p->d); a.rot = static_cast<int>(p->rot); a.pairs = r.pairs;
+  a.tile = r.tile; a.heads_per_block = r.heads_per_block; a.amp = p->amplitude;
+  return a;
+}
+
+// ------------------------------------------------------------------ window attention
+constexpr int kWattnFarRows = 1024;   // query rows of a sink tile's far part
+
+struct WattnDims {
+  int64_t B, H, Hkv, T, Tq, d, DP;
+  int window, sinks, dtype;
+  int bn, sink_tiles, parts, key_tiles;   // of the keys' gradients
+};
+
+static int wattn_validate(const lact_swa_sink_problem* p, WattnDims& D) {
+  if (!p || p->B < 1 || p->H < 1 || p->Hkv < 1 || p->T < 1 || p->Tq < 1 || p->d < 1) return LACT_EINVAL;
+  if (p->dtype != LACT_F32 && p->dtype != LACT_BF16) return LACT_EINVAL;
+  if (p->H % p->Hkv != 0 || p->Tq > p->T || p->d % 8 != 0 || p->d > 256) return LACT_EINVAL;
+  if (p->window < 1 || p->sinks < 0 || !std::isfinite(p->scale)) return LACT_EINVAL;
+  if (p->B * p->H > 65535 || p->T > (int64_t(1) << 24)) return LACT_EINVAL;
+  D.B = p->B; D.H = p->H; D.Hkv = p->Hkv; D.T = p->T; D.Tq = p->Tq; D.d = p->d;
+  D.DP = rup(p->d, 64);
+  D.window = static_cast<int>(std::min(p->window, p->T));
+  D.sinks = static_cast<int>(std::min(p->sinks, p->T));
+  D.dtype = p->dtype;
+  D.bn = D.dtype == LACT_F32 ? kSimtM : 128;
+  D.key_tiles = static_cast<int>(cdiv(D.T, D.bn));
+  D.sink_tiles = static_cast<int>(cdiv(D.sinks, D.bn));
+  const int far = far_parts(D.bn, D.window, static_cast<int>(D.T), kWattnFarRows);
+  if (far == 0) D.sink_tiles = 0;   // the window reaches every query: no far part
+  D.parts = 1 + far;
+  return LACT_OK;
+}
+
+struct WattnBufs {
+  float *delta, *part;
+};
+static void wattn_bwd_plan(const WattnDims& D, Bump& bp, WattnBufs& b) {
+  b.delta = bp.take<float>(D.B * D.H * D.Tq);
+  b.part = bp.take<float>(D.B * D.Hkv * D.sink_tiles * D.parts * 2 * D.bn * D.DP);
+}
+static size_t wattn_bwd_workspace(const WattnDims& D) {
+  Bump bp{0, 0};
+  WattnBufs b;
+  wattn_bwd_plan(D, bp, b);
+  return static_cast<size_t>(rup(static_cast<int64_t>(bp.off), 256));
+}
+
+static WattnParams wattn_params(const WattnDims& D, float scale, const int32_t* lengths, const float* lse) {
+  WattnParams a;
+  std::memset(&a, 0, sizeof(a));
+  a.lse = const_cast<float*>(lse); a.lengths = lengths; a.scale = scale;
+  a.B = static_cast<int>(D.B); a.H = static_cast<int>(D.H); a.Hkv = static_cast<int>(D.Hkv);
+  a.group = static_cast<int>(D.H / D.Hkv); a.T = static_cast<int>(D.T); a.Tq = static_cast<int>(D.Tq);
+  a.d = static_cast<int>(D.d); a.window = D.window; a.sinks = D.sinks; a.far_rows = kWattnFarRows;
+  return a;
+}
+
+template <int DP>
+static cudaError_t wattn_fwd_f32(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
+  static bool done[64] = {};
+  const cudaError_t e = set_smem(k_wattn_fwd_f32<DP>, SimtCfg<DP>::kFwdSmem, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(cdiv(D.Tq, kSimtM)), static_cast<unsigned>(D.B * D.H));
+  return launch_pdl(k_wattn_fwd_f32<DP>, grid, dim3(kSimtThreads), SimtCfg<DP>::kFwdSmem, st, a);
+}
+template <int DP>
+static cudaError_t wattn_dq_f32(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
+  static bool done[64] = {};
+  static_assert(SimtCfg<DP>::kBwdSmem <= kMaxSmemPerBlock, "dynamic shared memory above the per-CTA limit");
+  const cudaError_t e = set_smem(k_wattn_dq_f32<DP>, SimtCfg<DP>::kBwdSmem, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(cdiv(D.Tq, kSimtM)), static_cast<unsigned>(D.B * D.H));
+  return launch_pdl(k_wattn_dq_f32<DP>, grid, dim3(kSimtThreads), SimtCfg<DP>::kBwdSmem, st, a);
+}
+template <int DP>
+static cudaError_t wattn_dkv_f32(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
+  static bool done[64] = {};
+  const cudaError_t e = set_smem(k_wattn_dkv_f32<DP>, SimtCfg<DP>::kBwdSmem, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(D.sink_tiles * D.parts + D.key_tiles - D.sink_tiles),
+                  static_cast<unsigned>(D.B * D.Hkv));
+  return launch_pdl(k_wattn_dkv_f32<DP>, grid, dim3(kSimtThreads), SimtCfg<DP>::kBwdSmem, st, a, D.sink_tiles, D.parts);
+}
+
+#define LACT_BY_DP(DPV, CALL)                  \
+  switch (DPV) {                               \
+    case 64: { constexpr int DP = 64; return CALL; }   \
+    case 128: { constexpr int DP = 128; return CALL; } \
+    case 192: { constexpr int DP = 192; return CALL; } \
+    default: { constexpr int DP = 256; return CALL; }  \
+  }
+
+static cudaError_t launch_wattn_delta(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(cdiv(D.B * D.H * D.Tq, 8), kPlanSMs * 16)));
+  return D.dtype == LACT_F32 ? launch_pdl(k_wattn_delta<float>, grid, dim3(256), 0, st, a)
+                             : launch_pdl(k_wattn_delta<__nv_bfloat16>, grid, dim3(256), 0, st, a);
+}
+static cudaError_t launch_wattn_sums(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
+  const int64_t n = D.B * D.Hkv * D.sink_tiles * 2 * D.bn * (D.DP / 4);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(cdiv(n, 256), kPlanSMs * 16)));
+  const int DP = static_cast<int>(D.DP);
+  return D.dtype == LACT_F32
+             ? launch_pdl(k_wattn_sink_sums<float>, grid, dim3(256), 0, st, a, D.sink_tiles, D.parts, D.bn, DP)
+             : launch_pdl(k_wattn_sink_sums<__nv_bfloat16>, grid, dim3(256), 0, st, a, D.sink_tiles, D.parts, D.bn, DP);
+}
+
+static void wattn_fwd_run(const WattnDims& D, const WattnParams& a, cudaStream_t st, Launcher& L) {
+  L.st = st;
+  L(K_WATTN_FWD, [&]() -> cudaError_t { LACT_BY_DP(D.DP, wattn_fwd_f32<DP>(D, a, st)) });
+}
+
+static void wattn_bwd_run(const WattnDims& D, const WattnParams& a, cudaStream_t st, Launcher& L) {
+  L.st = st;
+  L(K_WATTN_ELEM, [&] { return launch_wattn_delta(D, a, st); });
+  L(K_WATTN_DQ, [&]() -> cudaError_t { LACT_BY_DP(D.DP, wattn_dq_f32<DP>(D, a, st)) });
+  L(K_WATTN_DKV, [&]() -> cudaError_t { LACT_BY_DP(D.DP, wattn_dkv_f32<DP>(D, a, st)) });
+  if (D.sink_tiles > 0) L(K_WATTN_ELEM, [&] { return launch_wattn_sums(D, a, st); });
+}
+
+// ------------------------------------------------------------------ single-token form
+static int decode_validate(const lact_swa_sink_problem* p) {
+  if (!p || p->B < 1 || p->H < 1 || p->Hkv < 1 || p->d < 1) return LACT_EINVAL;
+  if (p->dtype != LACT_F32 && p->dtype != LACT_BF16) return LACT_EINVAL;
+  if (p->H % p->Hkv != 0 || p->d % 8 != 0 || p->d > 256) return LACT_EINVAL;
+  if (p->window < 1 || p->sinks < 0 || !std::isfinite(p->scale)) return LACT_EINVAL;
+  if (p->window > (int64_t(1) << 30) || p->sinks > (int64_t(1) << 30)) return LACT_EINVAL;
+  if (p->B * p->H > 65535) return LACT_EINVAL;
+  return LACT_OK;
+}
+
+// CTAs of one (sequence, key head): doubled while the whole grid would leave
+// SMs idle and each CTA keeps a block of 16 slots for each of its warps.
+static int decode_ranks(int64_t items, int64_t slots) {
+  int r = 1;
+  while (r < 8 && items * r < kPlanSMs && slots > static_cast<int64_t>(r) * kDecWarps * 16) r *= 2;
+  return r;
+}
+
+template <class F>
+static cudaError_t launch_decode_as(F* kernel, int smem, bool (&done)[64], const DecodeParams& a, int64_t items,
+                                    cudaStream_t st) {
+  cudaError_t e = set_smem(kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  const int ranks = decode_ranks(items, static_cast<int64_t>(a.sinks) + a.window);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks, static_cast<unsigned>(items));
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int DP>
+static cudaError_t launch_decode(int dtype, const DecodeParams& a, int64_t items, cudaStream_t st) {
+  constexpr int smem = (2 * kDecWarps * kDecHeads + kDecWarps * kDecHeads * DP) * 4;
+  if (dtype == LACT_BF16) {
+    static bool done[64] = {};
+    return launch_decode_as(k_wattn_decode_bf16<DP>, smem, done, a, items, st);
+  }
+  const int heads = std::min(a.group, kDecHeads);
+  static bool done1[64] = {}, done4[64] = {}, done8[64] = {};
+  if (heads == 1) return launch_decode_as(k_wattn_decode_f32<DP, 1>, smem, done1, a, items, st);
+  if (heads <= 4) return launch_decode_as(k_wattn_decode_f32<DP, 4>, smem, done4, a, items, st);
+  return launch_decode_as(k_wattn_decode_f32<DP, 8>, smem, done8, a, items, st);
+}
+
+static cudaError_t launch_decode_any(int64_t DPV, int dtype, const DecodeParams& a, int64_t items, cudaStream_t st) {
+  LACT_BY_DP(DPV, launch_decode<DP>(dtype, a, items, st))
+}
+
+}  // namespace lact
+
+// ------------------------------------------------------------------ entry points
+extern "C" {
+
+size_t lact_rotary_bwd_workspace_bytes(const lact_rotary_problem* p) {
+  return lact::rotary_validate(p) == LACT_OK ? lact::rotary_bwd_workspace(p) : 0;
+}
+
+int lact_rotary_fwd(const lact_rotary_problem* p, const lact_tensor4* q, const lact_tensor4* k, const double* freqs,
+                    const int32_t* positions, const float* q_scale, const float* q_offset, const float* k_scale,
+                    const float* k_offset, const lact_tensor4* q_out, const lact_tensor4* k_out, void* stream) {
+  using namespace lact;
+  const int rc = rotary_validate(p);
+  if (rc != LACT_OK) return rc;
+  const int esz = p->dtype == LACT_BF16 ? 2 : 4;
+  const Extent4 eq{p->B, p->H, p->T, p->d}, ek{p->B, p->Hkv, p->T, p->d};
+  const bool has_k = p->Hkv > 0, affine = q_scale != nullptr;
+  if (!freqs || !aligned16(freqs) || !view_ok(q, eq, esz) || !view_ok(q_out, eq, esz)) return LACT_EINVAL;
+  if (has_k && (!view_ok(k, ek, esz) || !view_ok(k_out, ek, esz))) return LACT_EINVAL;
+  const float* params[] = {q_scale, q_offset, k_scale, k_offset};
+  for (int i = 0; i < (has_k ? 4 : 2); ++i)
+    if ((params[i] != nullptr) != affine || !aligned16(params[i])) return LACT_EINVAL;
+  const RotaryDims r = rotary_dims(p, false);
+  RotaryParams a = rotary_params(p, r, freqs, positions);
+  a.xq = view4(q, eq); a.yq = view4(q_out, eq);
+  if (!injective(a.yq, eq)) return LACT_EINVAL;
+  if (!same(a.xq, a.yq, eq) && !apart(a.xq, eq, a.yq, eq, esz)) return LACT_EINVAL;
+  if (has_k) {
+    a.xk = view4(k, ek); a.yk = view4(k_out, ek);
+    if (!injective(a.yk, ek) || !apart(a.yq, eq, a.yk, ek, esz) || !apart(a.yq, eq, a.xk, ek, esz) ||
+        !apart(a.xq, eq, a.yk, ek, esz) || (!same(a.xk, a.yk, ek) && !apart(a.xk, ek, a.yk, ek, esz)))
+      return LACT_EINVAL;
+  }
+  a.q_scale = q_scale; a.q_offset = q_offset; a.k_scale = k_scale; a.k_offset = k_offset;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Launcher L{false, st};
+  L(K_ROTARY, [&] { return affine ? launch_rotary_any<false, true>(p, r, a, st) : launch_rotary_any<false, false>(p, r, a, st); });
+  return L.err;
+}
+
+int lact_rotary_bwd(const lact_rotary_problem* p, const lact_tensor4* dq_out, const lact_tensor4* dk_out,
+                    const double* freqs, const int32_t* positions, const lact_tensor4* q, const lact_tensor4* k,
+                    const float* q_scale, const float* k_scale, const lact_tensor4* dq, const lact_tensor4* dk,
+                    float* dq_scale, float* dq_offset, float* dk_scale, float* dk_offset, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  using namespace lact;
+  const int rc = rotary_validate(p);
+  if (rc != LACT_OK) return rc;
+  const int esz = p->dtype == LACT_BF16 ? 2 : 4;
+  const Extent4 eq{p->B, p->H, p->T, p->d}, ek{p->B, p->Hkv, p->T, p->d};
+  const bool has_k = p->Hkv > 0, affine = q_scale != nullptr;
+  if (!freqs || !aligned16(freqs) || !view_ok(dq_out, eq, esz) || !view_ok(dq, eq, esz)) return LACT_EINVAL;
+  if (has_k && (!view_ok(dk_out, ek, esz) || !view_ok(dk, ek, esz))) return LACT_EINVAL;
+  if (has_k && (k_scale != nullptr) != affine) return LACT_EINVAL;
+  if (!aligned16(q_scale) || !aligned16(k_scale)) return LACT_EINVAL;
+  const RotaryDims r = rotary_dims(p, affine);
+  RotaryParams a = rotary_params(p, r, freqs, positions);
+  a.yq = view4(dq_out, eq); a.dq = view4(dq, eq);
+  if (!injective(a.dq, eq) || (!same(a.yq, a.dq, eq) && !apart(a.yq, eq, a.dq, eq, esz))) return LACT_EINVAL;
+  if (has_k) {
+    a.yk = view4(dk_out, ek); a.dk = view4(dk, ek);
+    if (!injective(a.dk, ek) || !apart(a.dq, eq, a.dk, ek, esz) || !apart(a.dq, eq, a.yk, ek, esz) ||
+        !apart(a.yq, eq, a.dk, ek, esz) || (!same(a.yk, a.dk, ek) && !apart(a.yk, ek, a.dk, ek, esz)))
+      return LACT_EINVAL;
+  }
+  if (affine) {
+    if (!view_ok(q, eq, esz) || (has_k && !view_ok(k, ek, esz))) return LACT_EINVAL;
+    a.xq = view4(q, eq);
+    if (!apart(a.xq, eq, a.dq, eq, esz)) return LACT_EINVAL;
+    if (has_k) {
+      a.xk = view4(k, ek);
+      if (!apart(a.xk, ek, a.dq, eq, esz) || !apart(a.xq, eq, a.dk, ek, esz) || !apart(a.xk, ek, a.dk, ek, esz))
+        return LACT_EINVAL;
+    }
+    float* g[] = {dq_scale, dq_offset, dk_scale, dk_offset};
+    for (int i = 0; i < (has_k ? 4 : 2); ++i) {
+      const int64_t n = (i < 2 ? p->H : p->Hkv) * p->d * 4;
+      if (!g[i] || !aligned16(g[i])) return LACT_EINVAL;
+      if (!apart_from(a.dq, eq, esz, g[i], n) || (has_k && !apart_from(a.dk, ek, esz, g[i], n))) return LACT_EINVAL;
+      for (int j = 0; j < i; ++j)
+        if (overlaps(g[i], n, g[j], (j < 2 ? p->H : p->Hkv) * p->d * 4)) return LACT_EINVAL;
+    }
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LACT_EINVAL;
+    if (workspace_bytes < rotary_bwd_workspace(p)) return LACT_ENOSPC;
+    a.partial = static_cast<float*>(workspace);
+  }
+  a.q_scale = q_scale; a.k_scale = k_scale;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Launcher L{false, st};
+  L(K_ROTARY, [&] { return affine ? launch_rotary_any<true, true>(p, r, a, st) : launch_rotary_any<true, false>(p, r, a, st); });
+  if (affine)
+    L(K_ROTARY_SUMS, [&] {
+      const int64_t n = 2 * (p->H + p->Hkv) * p->d;
+      return launch_pdl(k_rotary_sums, dim3(static_cast<unsigned>(cdiv(n, 32))), dim3(512), 0, st,
+                        static_cast<const float*>(a.partial), static_cast<int>(r.tiles), a.H, a.Hkv, a.d, dq_scale,
+                        dq_offset, dk_scale, dk_offset);
+    });
+  return L.err;
+}
+
+int lact_swa_sink_fwd(const lact_swa_sink_problem* p, const lact_tensor4* q, const lact_tensor4* k,
+                      const lact_tensor4* v, const int32_t* lengths, const lact_tensor4* out, float* lse,
+                      void* stream) {
+  using namespace lact;
+  WattnDims D;
+  const int rc = wattn_validate(p, D);
+  if (rc != LACT_OK) return rc;
+  if (D.dtype == LACT_BF16) return LACT_EINVAL;   // no kernel yet
+  const int esz = D.dtype == LACT_BF16 ? 2 : 4;
+  const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
+  if (!view_ok(q, eq, esz) || !view_ok(k, ek, esz) || !view_ok(v, ek, esz) || !view_ok(out, eq, esz)) return LACT_EINVAL;
+  if (!lse || !aligned16(lse)) return LACT_EINVAL;
+  WattnParams a = wattn_params(D, p->scale, lengths, lse);
+  a.q = view4(q, eq); a.k = view4(k, ek); a.v = view4(v, ek); a.out = view4(out, eq);
+  if (!injective(a.out, eq) || !apart(a.q, eq, a.out, eq, esz) || !apart(a.k, ek, a.out, eq, esz) ||
+      !apart(a.v, ek, a.out, eq, esz))
+    return LACT_EINVAL;
+  const int64_t n = D.B * D.H * D.Tq * 4;
+  if (!apart_from(a.q, eq, esz, lse, n) || !apart_from(a.k, ek, esz, lse, n) || !apart_from(a.v, ek, esz, lse, n) ||
+      !apart_from(a.out, eq, esz, lse, n))
+    return LACT_EINVAL;
+  Launcher L{false, static_cast<cudaStream_t>(stream)};
+  wattn_fwd_run(D, a, static_cast<cudaStream_t>(stream), L);
+  return L.err;
+}
+
+size_t lact_swa_sink_bwd_workspace_bytes(const lact_swa_sink_problem* p) {
+  lact::WattnDims D;
+  return lact::wattn_validate(p, D) == LACT_OK ? lact::wattn_bwd_workspace(D) : 0;
+}
+
+int lact_swa_sink_bwd(const lact_swa_sink_problem* p, const lact_tensor4* q, const lact_tensor4* k,
+                      const lact_tensor4* v, const lact_tensor4* out, const float* lse, const lact_tensor4* dout,
+                      const int32_t* lengths, const lact_tensor4* dq, const lact_tensor4* dk, const lact_tensor4* dv,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace lact;
+  WattnDims D;
+  const int rc = wattn_validate(p, D);
+  if (rc != LACT_OK) return rc;
+  if (D.dtype == LACT_BF16) return LACT_EINVAL;   // no kernel yet
+  const int esz = D.dtype == LACT_BF16 ? 2 : 4;
+  const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
+  const lact_tensor4* qs[] = {q, out, dout, dq};
+  const lact_tensor4* ks[] = {k, v, dk, dv};
+  for (const lact_tensor4* x : qs)
+    if (!view_ok(x, eq, esz)) return LACT_EINVAL;
+  for (const lact_tensor4* x : ks)
+    if (!view_ok(x, ek, esz)) return LACT_EINVAL;
+  if (!lse || !aligned16(lse)) return LACT_EINVAL;
+  WattnParams a = wattn_params(D, p->scale, lengths, lse);
+  a.q = view4(q, eq); a.k = view4(k, ek); a.v = view4(v, ek); a.out = view4(out, eq); a.dout = view4(dout, eq);
+  a.dq = view4(dq, eq); a.dk = view4(dk, ek); a.dv = view4(dv, ek);
+  const View4 in[] = {a.q, a.out, a.dout, a.k, a.v}, res[] = {a.dq, a.dk, a.dv};
+  for (int i = 0; i < 3; ++i) {
+    const Extent4& e = i ? ek : eq;
+    if (!injective(res[i], e) || !apart_from(res[i], e, esz, lse, D.B * D.H * D.Tq * 4)) return LACT_EINVAL;
+    for (int j = 0; j < 5; ++j)
+      if (!apart(res[i], e, in[j], j < 3 ? eq : ek, esz)) return LACT_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (!apart(res[i], e, res[j], j ? ek : eq, esz)) return LACT_EINVAL;
+  }
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LACT_EINVAL;
+  if (workspace_bytes < wattn_bwd_workspace(D)) return LACT_ENOSPC;
+  Bump bp{reinterpret_cast<uintptr_t>(workspace), 0};
+  WattnBufs b;
+  wattn_bwd_plan(D, bp, b);
+  a.delta = b.delta; a.part = b.part;
+  Launcher L{false, static_cast<cudaStream_t>(stream)};
+  wattn_bwd_run(D, a, static_cast<cudaStream_t>(stream), L);
+  return L.err;
+}
+
+int lact_swa_sink_decode(const lact_swa_sink_problem* p, const lact_tensor4* q, const lact_tensor4* k,
+                         const lact_tensor4* v, void* k_cache, void* v_cache, const int32_t* seen,
+                         const lact_tensor4* out, void* stream) {
+  using namespace lact;
+  const int rc = decode_validate(p);
+  if (rc != LACT_OK) return rc;
+  if (p->T != 1 || p->Tq != 1) return LACT_EINVAL;
+  const int esz = p->dtype == LACT_BF16 ? 2 : 4;
+  const Extent4 eq{p->B, p->H, 1, p->d}, ek{p->B, p->Hkv, 1, p->d};
+  if (!view_ok(q, eq, esz) || !view_ok(out, eq, esz) || !view_ok(k, ek, esz) || !view_ok(v, ek, esz)) return LACT_EINVAL;
+  if (!seen || !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return LACT_EINVAL;
+  DecodeParams a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = view4(q, eq); a.out = view4(out, eq); a.kn = view4(k, ek); a.vn = view4(v, ek);
+  const int64_t bytes = p->B * p->Hkv * (p->sinks + p->window) * p->d * esz;
+  if (overlaps(k_cache, bytes, v_cache, bytes) || !injective(a.out, eq)) return LACT_EINVAL;
+  if (!apart(a.out, eq, a.q, eq, esz) || !apart(a.out, eq, a.kn, ek, esz) || !apart(a.out, eq, a.vn, ek, esz))
+    return LACT_EINVAL;
+  for (void* c : {k_cache, v_cache})
+    if (!apart_from(a.q, eq, esz, c, bytes) || !apart_from(a.out, eq, esz, c, bytes) ||
+        !apart_from(a.kn, ek, esz, c, bytes) || !apart_from(a.vn, ek, esz, c, bytes))
+      return LACT_EINVAL;
+  a.kc = k_cache; a.vc = v_cache; a.seen = seen; a.scale = p->scale;
+  a.H = static_cast<int>(p->H); a.Hkv = static_cast<int>(p->Hkv); a.group = static_cast<int>(p->H / p->Hkv);
+  a.d = static_cast<int>(p->d); a.window = static_cast<int>(p->window); a.sinks = static_cast<int>(p->sinks);
+  a.hgroups = static_cast<int>(cdiv(a.group, kDecHeads));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Launcher L{false, st};
+  L(K_WATTN_DECODE, [&] { return launch_decode_any(rup(p->d, 64), p->dtype, a, p->B * p->Hkv * a.hgroups, st); });
+  return L.err;
+}
+
+int lact_swa_cache_fill(const lact_swa_sink_problem* p, const lact_tensor4* k, const lact_tensor4* v,
+                        const int32_t* lengths, void* k_cache, void* v_cache, void* stream) {
+  using namespace lact;
+  const int rc = decode_validate(p);
+  if (rc != LACT_OK) return rc;
+  if (p->T < 1 || p->T > (int64_t(1) << 24)) return LACT_EINVAL;
+  const int esz = p->dtype == LACT_BF16 ? 2 : 4;
+  const Extent4 ek{p->B, p->Hkv, p->T, p->d};
+  if (!view_ok(k, ek, esz) || !view_ok(v, ek, esz)) return LACT_EINVAL;
+  if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return LACT_EINVAL;
+  FillParams a;
+  std::memset(&a, 0, sizeof(a));
+  a.k = view4(k, ek); a.v = view4(v, ek);
+  const int64_t slots = p->sinks + p->window, bytes = p->B * p->Hkv * slots * p->d * esz;
+  if (overlaps(k_cache, bytes, v_cache, bytes)) return LACT_EINVAL;
+  for (void* c : {k_cache, v_cache})
+    if (!apart_from(a.k, ek, esz, c, bytes) || !apart_from(a.v, ek, esz, c, bytes)) return LACT_EINVAL;
+  a.kc = k_cache; a.vc = v_cache; a.lengths = lengths;
+  a.n = p->B * p->Hkv * std::min(p->T, slots);
+  a.Hkv = static_cast<int>(p->Hkv); a.T = static_cast<int>(p->T); a.row_vecs = static_cast<int>(p->d * esz / 16);
+  a.window = static_cast<int>(p->window); a.sinks = static_cast<int>(p->sinks); a.esz = esz;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Launcher L{false, st};
+  L(K_WATTN_ELEM, [&] {
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(cdiv(a.n * a.row_vecs, 256), kPlanSMs * 16)));
+    return launch_pdl(k_wattn_fill, grid, dim3(256), 0, st, a);
+  });
+  return L.err;
+}
+
+}  // extern "C"

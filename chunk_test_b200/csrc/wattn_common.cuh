@@ -1,0 +1,67 @@
+// wattn_common.cuh -- what the kernels of the window attention with sinks
+// share: the problem, its mask and the split of the sinks' gradients.
+//
+// Key j is visible to the query at position i (query t sits at T - Tq + t)
+// when j <= i and (j > i - window or j < sinks), both below the sequence's
+// length.  out_i = sum_j softmax_j(scale q_i . k_j) v_j over the visible keys,
+// lse_i = log sum_j exp(scale q_i . k_j); a row at or past its sequence's
+// length gets out 0 and lse -inf and has no gradient.  Query head h reads key
+// head h / (H / Hkv).
+#pragma once
+
+#include "rotary_kernels.cuh"
+
+namespace lact {
+
+struct WattnParams {
+  View4 q, k, v, out, dout;          // forward: out is written; backward: read
+  View4 dq, dk, dv;
+  float* lse;                        // [B, H, Tq]
+  const int* lengths;                // [B] or null: T
+  float* delta;                      // backward: rowsum(dout * out) [B, H, Tq]
+  float* part;                       // backward: the sink tiles' partial dk, dv
+  float scale;
+  int B, H, Hkv, group, T, Tq, d;    // group = H / Hkv
+  int window, sinks;                 // each at most T
+  int far_rows;                      // query rows of one far part of a sink tile
+};
+
+__device__ __forceinline__ int seq_len(const WattnParams& p, int b) {
+  return p.lengths ? max(0, min(p.lengths[b], p.T)) : p.T;
+}
+
+// Gradients of keys [kt BN, (kt + 1) BN): the queries that see any of them
+// through the window are positions [kt BN, kt BN + BN - 1 + window).  A tile
+// that holds sink keys is also seen by every later query; those positions are
+// cut into far parts of `far_rows`, one CTA each, and the tile's partial sums
+// are joined in a fixed order afterwards.  Part 0 is the near one.
+struct KeyPart {
+  int lo, hi;      // query positions
+};
+__host__ __device__ __forceinline__ int near_end(int kt, int bn, int window, int T) {
+  const int64_t e = static_cast<int64_t>(kt) * bn + bn - 1 + window;
+  return e < T ? static_cast<int>(e) : T;
+}
+// far parts of a sink tile; the same for each sink tile: positions from the
+// first tile's near end on (a later tile's parts that its near part covers
+// are empty)
+__host__ __device__ __forceinline__ int far_parts(int bn, int window, int T, int far_rows) {
+  const int e = near_end(0, bn, window, T);
+  return (T - e + far_rows - 1) / far_rows;
+}
+__host__ __device__ __forceinline__ KeyPart key_part(int kt, int part, int bn, int window, int T, int far_rows) {
+  KeyPart r;
+  const int near = near_end(kt, bn, window, T);
+  if (part == 0) {
+    r.lo = kt * bn;
+    r.hi = near;
+  } else {
+    const int64_t lo = near_end(0, bn, window, T) + static_cast<int64_t>(part - 1) * far_rows;
+    const int64_t hi = lo + far_rows;
+    r.lo = static_cast<int>(lo > near ? lo : near);
+    r.hi = static_cast<int>(hi < T ? hi : T);
+  }
+  return r;
+}
+
+}  // namespace lact

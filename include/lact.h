@@ -357,6 +357,130 @@ int lact_swa_fwd(const lact_swa_problem* p, const void* q, const void* k, const 
                  const float* k_scale, const float* k_offset,
                  void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention half of the block with positions, first tokens that stay
+ * visible, its gradient and its serving form.
+ *
+ * A [B, heads, T, d] tensor: `data` points at element (0, 0, 0, 0), channels
+ * are contiguous, the other strides are in elements, positive, and multiples
+ * of 16 bytes (the stride of a dimension of length 1 is ignored).  So a
+ * projection's [B, T, heads, d] result, or its slice of a packed one, is read
+ * and written in place.  Data pointers are 16-byte aligned device pointers.
+ * Outputs may not overlap themselves, one another or an input, except where
+ * an entry point says so; two tensors with the same row pitch (stride_t) in
+ * different columns of one packed buffer do not overlap. */
+typedef struct lact_tensor4 {
+  void* data;
+  int64_t stride_b, stride_h, stride_t;
+} lact_tensor4;
+
+/* Rotary positions of the block's queries [B, H, T, d] and keys
+ * [B, Hkv, T, d] (Hkv = 0: queries alone, every k argument NULL), after the
+ * block's per head and channel scales and offsets ([P1 §1.1]):
+ *   x' = x * scale[h] + offset[h]   (all of them given, or none),
+ *   y_a = amplitude (x'_a cos t - x'_b sin t),
+ *   y_b = amplitude (x'_b cos t + x'_a sin t),  t = position * freqs[i]
+ * for the pairs i < rot / 2: channels (2i, 2i + 1) when `interleaved`, else
+ * (i, i + rot / 2); channels from `rot` on are x'.  freqs: DEVICE [rot / 2]
+ * float64, radians per position (16-byte aligned); scaled for long contexts
+ * by the caller.  positions: DEVICE [B, T] int32, or NULL for start + t.
+ * Scales and offsets: [H, d] and [Hkv, d] float32.  Angles are formed in 64
+ * bits, the rest in 32, results rounded once to dtype (LACT_F32 or
+ * LACT_BF16).  q_out may be q itself and k_out k itself (in place).
+ * Limits: d a multiple of 8 up to 512, rot even, 2 <= rot <= d,
+ * B * (H + Hkv) <= 65535, T <= 2^30, 0 <= start <= 2^40. */
+typedef struct lact_rotary_problem {
+  int64_t B, H, Hkv, T, d, rot, start;
+  int32_t interleaved;
+  int32_t dtype;
+  float amplitude;
+  int32_t reserved;
+} lact_rotary_problem;
+
+int lact_rotary_fwd(const lact_rotary_problem* p, const lact_tensor4* q, const lact_tensor4* k,
+                    const double* freqs, const int32_t* positions,
+                    const float* q_scale, const float* q_offset,
+                    const float* k_scale, const float* k_offset,
+                    const lact_tensor4* q_out, const lact_tensor4* k_out, void* stream);
+
+/* Device scratch of lact_rotary_bwd with scales (0 if *p is invalid). */
+size_t lact_rotary_bwd_workspace_bytes(const lact_rotary_problem* p);
+
+/* Its backward: dq_out, dk_out are the gradients of q_out, k_out; dq, dk
+ * (dtype) those of q, k, in place if they are the same tensors.  With scales
+ * (q_scale, k_scale), q and k are the forward's inputs and dq_scale,
+ * dq_offset [H, d], dk_scale, dk_offset [Hkv, d] float32 receive the
+ * parameters' gradients, summed in 32 bits in a fixed order (the same bits on
+ * every run), through `workspace` (256-byte aligned); without, those
+ * arguments and q, k, workspace are ignored. */
+int lact_rotary_bwd(const lact_rotary_problem* p, const lact_tensor4* dq_out, const lact_tensor4* dk_out,
+                    const double* freqs, const int32_t* positions,
+                    const lact_tensor4* q, const lact_tensor4* k,
+                    const float* q_scale, const float* k_scale,
+                    const lact_tensor4* dq, const lact_tensor4* dk,
+                    float* dq_scale, float* dq_offset, float* dk_scale, float* dk_offset,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sliding-window attention with sinks: the first `sinks` tokens stay visible
+ * to every later one.  q [B, H, Tq, d], k, v [B, Hkv, T, d], H a multiple of
+ * Hkv (query head h reads key head h / (H / Hkv)), Tq <= T: the queries are
+ * the last Tq positions.  Key j is visible to the query at position i when
+ * j <= i and (j > i - window or j < sinks) and both are below lengths[b]
+ * (DEVICE [B] int32, clamped to 0..T; NULL: T).
+ *   out_i = sum_j softmax_j(scale q_i . k_j) v_j      [B, H, Tq, d], dtype
+ *   lse_i = log sum_j exp(scale q_i . k_j)            [B, H, Tq], float32
+ * A row at or behind its sequence's length has out 0 and lse -inf, and what
+ * k, v and q hold there is never used.  Values below the length have to be
+ * finite: inside a tile a masked key's probability is 0, and 0 times an
+ * infinite value is not.
+ * dtype LACT_BF16: products on the tensor cores, scores, statistics and sums
+ * in 32 bits, probabilities rounded to bf16 for the second product.
+ * LACT_F32: all in 32 bits on the CUDA cores.
+ * Limits: d a multiple of 8 up to 256, B * H <= 65535, T <= 2^24, any window
+ * >= 1 and sinks >= 0. */
+typedef struct lact_swa_sink_problem {
+  int64_t B, H, Hkv, T, Tq, d, window, sinks;
+  float scale;      /* of the scores, usually 1 / sqrt(d) */
+  int32_t dtype;
+} lact_swa_sink_problem;
+
+int lact_swa_sink_fwd(const lact_swa_sink_problem* p, const lact_tensor4* q, const lact_tensor4* k,
+                      const lact_tensor4* v, const int32_t* lengths,
+                      const lact_tensor4* out, float* lse, void* stream);
+
+/* Device scratch of lact_swa_sink_bwd (0 if *p is invalid). */
+size_t lact_swa_sink_bwd_workspace_bytes(const lact_swa_sink_problem* p);
+
+/* Its backward: the gradients dq, dk, dv (dtype) for the gradient `dout` of
+ * out, from the forward's inputs, out and lse.  No atomics: the same bits on
+ * every run.  Rows behind a sequence's length get 0.  `workspace`: device
+ * scratch, 256-byte aligned. */
+int lact_swa_sink_bwd(const lact_swa_sink_problem* p, const lact_tensor4* q, const lact_tensor4* k,
+                      const lact_tensor4* v, const lact_tensor4* out, const float* lse,
+                      const lact_tensor4* dout, const int32_t* lengths,
+                      const lact_tensor4* dq, const lact_tensor4* dk, const lact_tensor4* dv,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same attention for one new token per sequence (T = Tq = 1) over a
+ * rolling cache.  k_cache, v_cache [B, Hkv, sinks + window, d], dense, dtype:
+ * the token at position p is in slot p when p < sinks, else in slot
+ * sinks + (p - sinks) % window.  seen: DEVICE [B] int32, the tokens each
+ * sequence has in its cache, so the new one's position.  The call writes the
+ * new k, v [B, Hkv, 1, d] into their slot and attends with q [B, H, 1, d] to
+ * every visible token, the new one included; out [B, H, 1, d].  `seen` is not
+ * advanced.  A sequence with seen < 0 is inactive: out 0, cache untouched.
+ * Slots that hold no token yet are not read.  One launch, no workspace.
+ * Limits: d a multiple of 8 up to 256, B * H <= 65535, window, sinks <= 2^30. */
+int lact_swa_sink_decode(const lact_swa_sink_problem* p, const lact_tensor4* q, const lact_tensor4* k,
+                         const lact_tensor4* v, void* k_cache, void* v_cache, const int32_t* seen,
+                         const lact_tensor4* out, void* stream);
+
+/* A prompt's k, v [B, Hkv, T, d] (T <= 2^24, lengths as above) into the
+ * caches: the sinks and the last `window` other tokens of each sequence, each
+ * in its slot; other slots keep what they hold.  H and Tq are not used. */
+int lact_swa_cache_fill(const lact_swa_sink_problem* p, const lact_tensor4* k, const lact_tensor4* v,
+                        const int32_t* lengths, void* k_cache, void* v_cache, void* stream);
+
 /* Waits for `stream`, then returns and clears the device status word of the
  * current device: LACT_OK, or LACT_ETIMEOUT if a bounded wait inside one of
  * this library's kernels gave up since the last call (its results are then

@@ -1,0 +1,256 @@
+"""CPU tests of the attention half's operators: the library's argument checks
+(found before anything is enqueued, so no GPU is needed), the wrappers' checks,
+the frequencies, and the oracle's gradients against differences."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import chunk_test_b200 as ct
+from chunk_test_b200 import _abi
+from oracle import attention_oracle as ao
+
+G = 1 << 32
+
+
+def t4(i, B=2, H=4, T=64, d=64, layout="bhtd", at=0):
+    s = (H * T * d, T * d, d) if layout == "bhtd" else (T * H * d, d, H * d)
+    return _abi.LactTensor4(G * (i + 1) + at, *s)
+
+
+def rot_problem(**kw):
+    a = dict(B=2, H=4, Hkv=2, T=64, d=64, rot=32, start=0, interleaved=0, dtype=1, amplitude=1.0, reserved=0)
+    a.update(kw)
+    return _abi.LactRotaryProblem(*a.values())
+
+
+def swa_problem(**kw):
+    a = dict(B=2, H=4, Hkv=2, T=64, Tq=64, d=64, window=16, sinks=4, scale=0.125, dtype=1)
+    a.update(kw)
+    return _abi.LactSwaSinkProblem(*a.values())
+
+
+def ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(B=0), dict(H=0), dict(Hkv=-1), dict(T=0), dict(d=0), dict(d=60), dict(d=520), dict(rot=0), dict(rot=31),
+    dict(rot=66), dict(start=-1), dict(interleaved=2), dict(dtype=2), dict(amplitude=math.nan), dict(B=70000),
+    dict(T=(1 << 30) + 1),
+])
+def test_rotary_problems_refused(bad):
+    p = rot_problem(**bad)
+    assert ct.lib().lact_rotary_bwd_workspace_bytes(ctypes.byref(p)) == 0
+    rc = ct.lib().lact_rotary_fwd(ctypes.byref(p), ref(t4(0)), ref(t4(1, H=2)), 9 * G, None, None, None, None, None,
+                                  ref(t4(2)), ref(t4(3, H=2)), None)
+    assert rc == ct.LACT_EINVAL
+
+
+def test_rotary_arguments_refused():
+    p = rot_problem()
+    lib = ct.lib()
+
+    def call(q=t4(0), k=t4(1, H=2), freqs=9 * G, par=(None,) * 4, qo=t4(2), ko=t4(3, H=2)):
+        return lib.lact_rotary_fwd(ctypes.byref(p), ref(q), ref(k), freqs, None, *par, ref(qo), ref(ko), None)
+
+    assert call(q=None) == ct.LACT_EINVAL
+    assert call(k=None) == ct.LACT_EINVAL
+    assert call(freqs=None) == ct.LACT_EINVAL
+    assert call(freqs=9 * G + 8) == ct.LACT_EINVAL
+    assert call(q=t4(0, at=8)) == ct.LACT_EINVAL                       # 16-byte alignment
+    assert call(par=(5 * G, 6 * G, 7 * G, None)) == ct.LACT_EINVAL     # all parameters or none
+    bent = t4(0)
+    bent.stride_t = 68                                                 # not a multiple of 16 bytes
+    assert call(q=bent) == ct.LACT_EINVAL
+    for name in ("stride_b", "stride_h", "stride_t"):
+        flat = t4(2)
+        setattr(flat, name, 0)                                         # one row for all
+        assert call(qo=flat) == ct.LACT_EINVAL
+    folded = t4(2)
+    folded.stride_h = 64                                               # heads over tokens
+    assert call(qo=folded) == ct.LACT_EINVAL
+    assert call(qo=t4(0, at=128)) == ct.LACT_EINVAL                    # shifted onto q
+    assert call(ko=t4(0)) == ct.LACT_EINVAL                            # k's result onto q
+    assert call(ko=t4(2)) == ct.LACT_EINVAL                            # both results in one place
+    # the backward with scales wants the workspace
+    nul = None
+    rc = lib.lact_rotary_bwd(ctypes.byref(p), ref(t4(0)), ref(t4(1, H=2)), 9 * G, nul, ref(t4(2)), ref(t4(3, H=2)),
+                             10 * G, 11 * G, ref(t4(4)), ref(t4(5, H=2)), 12 * G, 13 * G, 14 * G, 15 * G, 16 * G,
+                             ctypes.c_size_t(8), nul)
+    assert rc == ct.LACT_ENOSPC
+    rc = lib.lact_rotary_bwd(ctypes.byref(p), ref(t4(0)), ref(t4(1, H=2)), 9 * G, nul, ref(t4(2)), ref(t4(3, H=2)),
+                             10 * G, 11 * G, ref(t4(4)), ref(t4(5, H=2)), 12 * G, 12 * G, 14 * G, 15 * G, 16 * G,
+                             ctypes.c_size_t(1 << 30), nul)
+    assert rc == ct.LACT_EINVAL                                        # two sums in one place
+
+
+@pytest.mark.parametrize("bad", [
+    dict(B=0), dict(H=0), dict(Hkv=0), dict(H=3), dict(T=0), dict(Tq=0), dict(Tq=65), dict(d=0), dict(d=60),
+    dict(d=264), dict(window=0), dict(sinks=-1), dict(scale=math.inf), dict(dtype=3), dict(B=20000),
+    dict(T=(1 << 24) + 1),
+])
+def test_attention_problems_refused(bad):
+    p = swa_problem(**bad)
+    lib = ct.lib()
+    assert lib.lact_swa_sink_bwd_workspace_bytes(ctypes.byref(p)) == 0
+    k, v = t4(1, H=2), t4(2, H=2)
+    assert lib.lact_swa_sink_fwd(ctypes.byref(p), ref(t4(0)), ref(k), ref(v), None, ref(t4(3)), 9 * G, None) == ct.LACT_EINVAL
+    assert lib.lact_swa_sink_bwd(ctypes.byref(p), ref(t4(0)), ref(k), ref(v), ref(t4(3)), 9 * G, ref(t4(4)), None,
+                                 ref(t4(5)), ref(t4(6, H=2)), ref(t4(7, H=2)), 10 * G, ctypes.c_size_t(1 << 40),
+                                 None) == ct.LACT_EINVAL
+
+
+def test_attention_arguments_refused():
+    p, lib = swa_problem(), ct.lib()
+
+    def fwd(q=t4(0), k=t4(1, H=2), v=t4(2, H=2), out=t4(3), lse=9 * G):
+        return lib.lact_swa_sink_fwd(ctypes.byref(p), ref(q), ref(k), ref(v), None, ref(out), lse, None)
+
+    for name in ("q", "k", "v", "out", "lse"):
+        assert fwd(**{name: None}) == ct.LACT_EINVAL, name
+    assert fwd(out=t4(0)) == ct.LACT_EINVAL
+    assert fwd(out=t4(1, H=2)) == ct.LACT_EINVAL
+    assert fwd(lse=G) == ct.LACT_EINVAL                                # onto q
+    assert fwd(k=t4(1, H=2, at=8)) == ct.LACT_EINVAL
+    flat = t4(1, H=2)
+    flat.stride_b = 0
+    assert fwd(k=flat) == ct.LACT_EINVAL
+
+    def bwd(ws=10 * G, n=1 << 40, dq=t4(5), dk=t4(6, H=2), dv=t4(7, H=2)):
+        return lib.lact_swa_sink_bwd(ctypes.byref(p), ref(t4(0)), ref(t4(1, H=2)), ref(t4(2, H=2)), ref(t4(3)), 9 * G,
+                                     ref(t4(4)), None, ref(dq), ref(dk), ref(dv), ws, ctypes.c_size_t(n), None)
+
+    assert bwd(ws=None) == ct.LACT_EINVAL
+    assert bwd(ws=10 * G + 16) == ct.LACT_EINVAL
+    assert bwd(n=16) == ct.LACT_ENOSPC
+    assert bwd(dq=t4(0)) == ct.LACT_EINVAL
+    assert bwd(dk=t4(7, H=2)) == ct.LACT_EINVAL                        # dk onto dv
+    assert bwd(dv=t4(1, H=2)) == ct.LACT_EINVAL                        # dv onto k
+
+
+def test_workspace_grows_with_the_sinks_only():
+    """Without sinks the backward keeps one float per query row; a sink tile
+    adds its parts, one near and one for each 1024 later query rows."""
+    def need(**kw):
+        return ct.lib().lact_swa_sink_bwd_workspace_bytes(ctypes.byref(swa_problem(**kw)))
+
+    assert need(T=4096, Tq=4096, sinks=0) == 2 * 4 * 4096 * 4
+    far = -(-(4096 - (127 + 16)) // 1024)
+    tile = 2 * 128 * 64 * 4
+    assert need(T=4096, Tq=4096, sinks=4) == 2 * 4 * 4096 * 4 + 2 * 2 * (1 + far) * tile
+    assert need(T=4096, Tq=4096, sinks=129) == 2 * 4 * 4096 * 4 + 2 * 2 * 2 * (1 + far) * tile
+    assert need(T=4096, Tq=4096, sinks=4, window=4096) == 2 * 4 * 4096 * 4
+
+
+@pytest.mark.parametrize("bad", [
+    dict(T=2), dict(Tq=2), dict(window=0), dict(sinks=-1), dict(d=100), dict(H=3), dict(dtype=5),
+    dict(window=(1 << 30) + 1),
+])
+def test_decode_problems_refused(bad):
+    p = swa_problem(**{**dict(T=1, Tq=1), **bad})
+    one = lambda i, H: t4(i, H=H, T=1)  # noqa: E731
+    rc = ct.lib().lact_swa_sink_decode(ctypes.byref(p), ref(one(0, 4)), ref(one(1, 2)), ref(one(2, 2)), 4 * G, 5 * G,
+                                       6 * G, ref(one(7, 4)), None)
+    assert rc == ct.LACT_EINVAL
+
+
+def test_decode_arguments_refused():
+    p = swa_problem(T=1, Tq=1)
+    one = lambda i, H: t4(i, H=H, T=1)  # noqa: E731
+
+    def call(q=one(0, 4), k=one(1, 2), v=one(2, 2), kc=4 * G, vc=5 * G, seen=6 * G, out=one(7, 4)):
+        return ct.lib().lact_swa_sink_decode(ctypes.byref(p), ref(q), ref(k), ref(v), kc, vc, seen, ref(out), None)
+
+    for name in ("q", "k", "v", "kc", "vc", "seen", "out"):
+        assert call(**{name: None}) == ct.LACT_EINVAL, name
+    assert call(vc=4 * G) == ct.LACT_EINVAL
+    assert call(kc=4 * G + 8) == ct.LACT_EINVAL
+    assert call(out=one(0, 4)) == ct.LACT_EINVAL
+    assert call(kc=G) == ct.LACT_EINVAL                                # the cache onto q
+    p2 = swa_problem()
+    assert ct.lib().lact_swa_cache_fill(ctypes.byref(p2), ref(t4(0, H=2)), None, None, 4 * G, 5 * G, None) == ct.LACT_EINVAL
+    assert ct.lib().lact_swa_cache_fill(ctypes.byref(p2), ref(t4(0, H=2)), ref(t4(1, H=2)), None, G, 5 * G,
+                                        None) == ct.LACT_EINVAL
+
+
+def test_wrappers_refuse_cpu_tensors_and_wrong_shapes():
+    q = torch.zeros(1, 2, 4, 64)
+    f = torch.zeros(8, dtype=torch.float64)
+    with pytest.raises(ValueError):
+        ct.rotary_fwd(q, q, f)
+    with pytest.raises(ValueError):
+        ct.swa_sink_fwd(q, q, q, 4)
+    with pytest.raises(ValueError):
+        ct.swa_sink_decode(q, q, q, q, q, f, 4)
+    with pytest.raises(ValueError):
+        ct.rotary_fwd(q[0], q, f)
+
+
+def test_frequencies():
+    f, a = ct.rotary_frequencies(8, device="cpu")
+    want = torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64)
+    assert a == 1.0 and torch.allclose(f, want, rtol=1e-14, atol=0)
+    assert torch.allclose(ct.rotary_frequencies(8, method="linear", factor=4.0, device="cpu")[0], want / 4, rtol=1e-14, atol=0)
+    g = ct.rotary_frequencies(8, method="base", factor=4.0, device="cpu")[0]
+    assert abs(float(g[0]) - 1.0) < 1e-14 and abs(float(g[-1]) * 4 - float(want[-1])) < 1e-14
+    # 2000 trained positions: the pairs turn 318, 31.8, 3.18 and 0.318 times
+    g, a = ct.rotary_frequencies(8, method="by_parts", factor=4.0, context=2000, low=1.0, high=32.0, device="cpu")
+    assert abs(a - (1 + 0.1 * math.log(4.0))) < 1e-14
+    assert float(g[0]) == float(want[0]) and abs(float(g[3]) * 4 - float(want[3])) < 1e-16
+    turns = 0.01 * 2000 / (2 * math.pi)
+    keep = (turns - 1) / 31
+    assert abs(float(g[2]) - 0.01 * (keep + (1 - keep) / 4)) < 1e-14
+    for bad in (dict(rot=7), dict(rot=0), dict(rot=8, method="other"), dict(rot=8, factor=0.5),
+                dict(rot=8, method="by_parts"), dict(rot=2, method="base")):
+        with pytest.raises(ValueError):
+            ct.rotary_frequencies(**{**dict(device="cpu"), **bad})
+
+
+def test_oracle_gradients_match_differences():
+    g = torch.Generator().manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=g, dtype=torch.float64)  # noqa: E731
+    q, k, v, dout = r(2, 4, 9, 8), r(2, 2, 13, 8), r(2, 2, 13, 8), r(2, 4, 9, 8)
+    args = dict(window=5, sinks=2, lengths=(13, 8))
+    w = ao.attention(q, k, v, dout=dout, **args)
+    f = lambda *x: float((ao.attention(*x, **args)["out"] * dout).sum())  # noqa: E731
+    for i, n in enumerate(("dq", "dk", "dv")):
+        e = r(*(q, k, v)[i].shape)
+        up, dn = [q, k, v], [q, k, v]
+        up[i], dn[i] = up[i] + 1e-5 * e, dn[i] - 1e-5 * e
+        d = (f(*up) - f(*dn)) / 2e-5
+        assert abs(d - float((w[n] * e).sum())) < 1e-7 * (1 + abs(d)), n
+    freqs = torch.tensor([1.0, 0.3, 0.05], dtype=torch.float64)
+    pos = torch.arange(9).expand(2, 9)
+    sc, of = r(4, 8), r(4, 8)
+    dx, ds, do, _, _ = ao.rotary_vjp(dout, freqs, pos, True, 1.1, q, sc)
+    fr = lambda a, b, c: float((ao.rotary(a, freqs, pos, True, 1.1, b, c) * dout).sum())  # noqa: E731
+    for i, got in enumerate((dx, ds, do)):
+        x = [q, sc, of]
+        e = r(*x[i].shape)
+        up, dn = list(x), list(x)
+        up[i], dn[i] = up[i] + 1e-5 * e, dn[i] - 1e-5 * e
+        d = (fr(*up) - fr(*dn)) / 2e-5
+        assert abs(d - float((got * e).sum())) < 1e-7 * (1 + abs(d)), i
+
+
+def test_oracle_is_plain_attention_where_the_window_covers_all():
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn((1, 2, 12, 8), generator=g, dtype=torch.float64) for _ in range(3))
+    s = (q @ k.transpose(-1, -2) / math.sqrt(8)).masked_fill(~torch.ones(12, 12).tril().bool(), -math.inf)
+    assert torch.allclose(ao.attention(q, k, v, 12)["out"], s.softmax(-1) @ v, rtol=1e-12, atol=1e-14)
+    assert torch.allclose(ao.attention(q, k, v, 3, 12)["out"], s.softmax(-1) @ v, rtol=1e-12, atol=1e-14)
+
+
+def test_oracle_decode_follows_the_sequence():
+    """The rolling cache, token by token, gives the attention over the whole sequence."""
+    g = torch.Generator().manual_seed(2)
+    T, window, sinks = 20, 6, 2
+    q, k, v = (torch.randn((1, n, T, 8), generator=g, dtype=torch.float64) for n in (4, 2, 2))
+    want = ao.attention(q, k, v, window, sinks)["out"]
+    kc = torch.full((1, 2, window + sinks, 8), math.nan, dtype=torch.float64)
+    vc = kc.clone()
+    for t in range(T):
+        o, _, kc, vc = ao.decode(q[:, :, t:t + 1], k[:, :, t:t + 1], v[:, :, t:t + 1], kc, vc, [t], window, sinks)
+        assert torch.allclose(o, want[:, :, t:t + 1], rtol=1e-12, atol=1e-14)

@@ -1,0 +1,182 @@
+"""GPU tests of the window attention with sinks, its backward and its
+single-token form against the fp64 definitions (oracle/attention_oracle.py).
+
+Bounds, elementwise, u = 2^-8 for bf16 (half a step), e the 32-bit part.
+Forward: the probabilities of the second product are rounded (u), the result
+is rounded (u):  |err| <= u (|out| + sum p |v|) + e (...).
+Backward: dv like the forward; ds is rounded (u |ds|), and out, which delta is
+formed from, was rounded and carries the forward's error, so delta is off by
+u sum |dout| (|out| + sum p |v|):  |dk err| <= u (|dk| + sum (|ds| + own) |q|),
+own = p scale times that sum without u.
+32-bit part: a score is off by 2^-23 d sum |q||k| scale at most (products
+exact, a chain of d additions), exp and the sums add a few 2^-23 each per
+addition: e = 2^-23 (d qk + n + 32) with qk the largest sum scale |q||k| and n
+the longest row or column of a sum.  float32 results have u = 2^-24 and no
+rounded factors; their products' terms are bounded by the sums themselves."""
+import math
+
+import pytest
+import torch
+
+import chunk_test_b200 as ct
+from oracle import attention_oracle as ao
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def make(B, H, Hkv, T, Tq, d, dtype, layout="bhtd", seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def one(heads, n):
+        if layout == "bthd":
+            return torch.randn((B, n, heads, d), generator=g, device="cuda").to(dtype).transpose(1, 2)
+        return torch.randn((B, heads, n, d), generator=g, device="cuda").to(dtype)
+
+    return one(H, Tq), one(Hkv, T), one(Hkv, T), one(H, Tq)
+
+
+def within(name, got, want, bound):
+    assert bool(torch.isfinite(got).all()), name
+    over = (got.double() - want).abs() / (bound + 1e-30)
+    assert float(over.max()) <= 1.0, (name, float(over.max()))
+
+
+def check_forward(got, lse, w, dtype, d, n):
+    e = 2.0 ** -23 * (d * w["qk"] + n + 32)
+    u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+    p_round = u if dtype == BF16 else 0.0
+    within("out", got, w["out"], u * w["out"].abs() + (1 + u) * (p_round + e) * w["pv"])
+    empty = torch.isinf(w["lse"])
+    assert torch.equal(torch.isinf(lse) & (lse < 0), empty)
+    assert bool((got[empty] == 0).all())
+    diff = (lse.double() - w["lse"])[~empty].abs()
+    assert diff.numel() == 0 or float((diff - 2.0 ** -23 * w["lse"][~empty].abs()).max()) <= e
+
+
+def check_backward(res, w, dtype, d, n):
+    e = 2.0 ** -23 * (2 * d * max(w["qk"], 1.0) + n + 64)
+    u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+    r = u if dtype == BF16 else 0.0
+    within("dq", res["dq"], w["dq"], u * w["dq"].abs() + (1 + u) * (r * w["adq"] + e * w["ddq"]))
+    within("dk", res["dk"], w["dk"], u * w["dk"].abs() + (1 + u) * (r * w["adk"] + e * w["ddk"]))
+    within("dv", res["dv"], w["dv"], u * w["dv"].abs() + (1 + u) * (r + e) * w["adv"])
+
+
+CASES = [
+    # B, H, Hkv, T, Tq, d, window, sinks, lengths, layout
+    (1, 1, 1, 1, 1, 64, 1, 0, None, "bhtd"),
+    (1, 2, 1, 2, 2, 64, 2, 0, None, "bhtd"),
+    (1, 2, 2, 77, 77, 64, 32, 1, None, "bhtd"),
+    (2, 2, 1, 128, 128, 64, 128, 0, None, "bthd"),
+    (1, 2, 1, 129, 129, 128, 64, 4, None, "bthd"),
+    (1, 3, 1, 300, 300, 128, 1, 3, None, "bhtd"),           # the token itself and three sinks
+    (1, 1, 1, 400, 400, 64, 100, 130, None, "bhtd"),        # sinks over more than one tile
+    (1, 2, 2, 511, 511, 80, 1000, 2, None, "bthd"),         # window longer than the sequence
+    (1, 2, 1, 640, 640, 256, 256, 0, None, "bhtd"),
+    (1, 1, 1, 700, 700, 192, 129, 16, None, "bthd"),
+    (1, 2, 1, 513, 200, 96, 130, 5, None, "bthd"),          # the last 200 positions
+    (1, 1, 1, 600, 1, 64, 70, 5, None, "bhtd"),             # the last position
+    (4, 2, 1, 260, 260, 64, 50, 4, (260, 0, 129, 1), "bhtd"),   # an empty sequence and ragged ends
+    (3, 4, 2, 300, 150, 128, 64, 8, (300, 170, 149), "bthd"),   # no query of the last one is left
+    (2, 6, 2, 1500, 1500, 64, 200, 4, None, "bhtd"),        # far parts of the sinks' gradients
+    (1, 1, 1, 2600, 2600, 8, 40, 200, (2500,), "bhtd"),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("B,H,Hkv,T,Tq,d,window,sinks,lengths,layout", CASES)
+def test_forward_and_backward(B, H, Hkv, T, Tq, d, window, sinks, lengths, layout, dtype):
+    q, k, v, dout = make(B, H, Hkv, T, Tq, d, dtype, layout, seed=T + d)
+    lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lens)
+    assert ct.status() == ct.LACT_OK
+    w = ao.attention(q, k, v, window, sinks, lengths, dout=dout)
+    check_forward(out, lse, w, dtype, d, min(T, window + sinks))
+    res = ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks, lengths=lens)
+    assert ct.status() == ct.LACT_OK
+    check_backward(res, w, dtype, d, T * (H // Hkv))
+
+
+@pytest.mark.parametrize("dtype", [F32])
+def test_padding_is_never_used(dtype):
+    """NaN and infinities behind the lengths, in every input: rows there get
+    out 0, lse -inf and gradients 0, the others are what they are without."""
+    B, H, Hkv, T, d, window, sinks = 3, 2, 1, 300, 64, 90, 4
+    lens = [300, 140, 3]
+    q, k, v, dout = make(B, H, Hkv, T, T, d, dtype)
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    clean = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lt)
+    g_clean = ct.swa_sink_bwd(q, k, v, *clean, dout, window, sinks, lengths=lt)
+    for x, bad in ((q, math.nan), (k, math.inf), (v, math.nan), (dout, -math.inf)):
+        for b, n in enumerate(lens):
+            x[b, :, n:] = bad
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lt)
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+    for b, n in enumerate(lens):
+        assert bool((out[b, :, n:] == 0).all()) and bool((lse[b, :, n:] == -math.inf).all())
+        out[b, :, n:] = math.nan
+    res = ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks, lengths=lt)
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(res[n], g_clean[n]), n
+        for b, m in enumerate(lens):
+            assert bool((res[n][b, :, m:] == 0).all())
+    assert ct.status() == ct.LACT_OK
+
+
+@pytest.mark.parametrize("dtype", [F32])
+def test_large_scores(dtype):
+    """Scores in the hundreds that rise along the keys, so the running maximum grows tile after tile."""
+    B, H, T, d, window = 1, 1, 700, 64, 600
+    q, k, v, dout = make(B, H, H, T, T, d, dtype)
+    q.fill_(1.0)
+    k.copy_((torch.arange(T, device="cuda", dtype=torch.float32) / 8).view(1, 1, T, 1).expand_as(k))
+    out, lse = ct.swa_sink_fwd(q, k, v, window, 2)
+    w = ao.attention(q, k, v, window, 2, dout=dout)
+    check_forward(out, lse, w, dtype, d, window)
+    check_backward(ct.swa_sink_bwd(q, k, v, out, lse, dout, window, 2), w, dtype, d, T)
+
+
+@pytest.mark.parametrize("dtype", [F32])
+def test_scale_outputs_and_repeats(dtype):
+    """An own scale, outputs in a [B, T, H, d] layout, a workspace with other
+    contents: the same bits each time, nothing written beside the outputs."""
+    B, H, Hkv, T, d, window, sinks = 2, 2, 1, 333, 64, 60, 4
+    q, k, v, dout = make(B, H, Hkv, T, T, d, dtype, "bthd")
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks, scale=0.3)
+    w = ao.attention(q, k, v, window, sinks, scale=0.3, dout=dout)
+    check_forward(out, lse, w, dtype, d, window + sinks)
+    first = ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks, scale=0.3)
+    check_backward(first, w, dtype, d, T * 2)
+
+    def packed(heads):
+        whole = torch.full((B, T, heads + 2, d), 7.0, dtype=dtype, device="cuda")
+        return whole, whole[:, :, 1:-1].transpose(1, 2)
+
+    (wo, o2), (wq, dq), (wk, dk), (wv, dv) = packed(H), packed(H), packed(Hkv), packed(Hkv)
+    ct.swa_sink_fwd(q, k, v, window, sinks, scale=0.3, out=o2)
+    ws = torch.full((ct.swa_sink_bwd_workspace_bytes(q, k, window, sinks),), 255, dtype=torch.uint8, device="cuda")
+    ct.swa_sink_bwd(q, k, v, o2, lse, dout, window, sinks, scale=0.3, dq=dq, dk=dk, dv=dv, workspace=ws)
+    for whole, got, ref in ((wo, o2, out), (wq, dq, first["dq"]), (wk, dk, first["dk"]), (wv, dv, first["dv"])):
+        assert torch.equal(got, ref)
+        assert bool((whole[:, :, 0] == 7).all()) and bool((whole[:, :, -1] == 7).all())
+
+
+def test_backward_is_the_forwards_gradient():
+    """Differences in 64 bits of the float32 kernel's own forward along a direction."""
+    q, k, v, dout = make(1, 2, 1, 150, 150, 64, F32, seed=5)
+    out, lse = ct.swa_sink_fwd(q, k, v, 40, 3)
+    res = ct.swa_sink_bwd(q, k, v, out, lse, dout, 40, 3)
+    h = 2.0 ** -6
+    for i, n in enumerate(("dq", "dk", "dv")):
+        x = [q, k, v]
+        e = torch.randn(x[i].shape, generator=torch.Generator(device="cuda").manual_seed(20 + i), device="cuda")
+        up, dn = list(x), list(x)
+        up[i], dn[i] = x[i] + h * e, x[i] - h * e
+        f = [float((ct.swa_sink_fwd(*y, 40, 3)[0].double() * dout.double()).sum()) for y in (up, dn)]
+        diff, want = (f[0] - f[1]) / (2 * h), float((res[n].double() * e.double()).sum())
+        # the third derivative's share, h^2 / 6 of terms as large as the gradient's, and 32-bit noise over h
+        size = float((res[n].double() * e.double()).abs().sum())
+        noise = 2.0 ** -20 * float((out.double() * dout.double()).abs().sum()) / h
+        assert abs(diff - want) <= h * h * size + noise, (n, diff, want)
+

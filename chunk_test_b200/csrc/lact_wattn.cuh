@@ -5,6 +5,8 @@
 #pragma once
 
 #include "wattn_decode.cuh"
+#include "wattn_bwd.cuh"
+#include "wattn_fwd.cuh"
 #include "wattn_simt.cuh"
 
 namespace lact {
@@ -176,7 +178,8 @@ static int wattn_validate(const lact_swa_sink_problem* p, WattnDims& D) {
   if (!p || p->B < 1 || p->H < 1 || p->Hkv < 1 || p->T < 1 || p->Tq < 1 || p->d < 1) return LACT_EINVAL;
   if (p->dtype != LACT_F32 && p->dtype != LACT_BF16) return LACT_EINVAL;
   if (p->H % p->Hkv != 0 || p->Tq > p->T || p->d % 8 != 0 || p->d > 256) return LACT_EINVAL;
-  if (p->window < 1 || p->sinks < 0 || !std::isfinite(p->scale)) return LACT_EINVAL;
+  if (p->window < 1 || p->sinks < 0 || !std::isfinite(p->scale) || !(p->scale > 0.f))
+    return LACT_EINVAL;
   if (p->B * p->H > 65535 || p->T > (int64_t(1) << 24)) return LACT_EINVAL;
   D.B = p->B; D.H = p->H; D.Hkv = p->Hkv; D.T = p->T; D.Tq = p->Tq; D.d = p->d;
   D.DP = rup(p->d, 64);
@@ -216,6 +219,42 @@ static WattnParams wattn_params(const WattnDims& D, float scale, const int32_t* 
   return a;
 }
 
+// 4-D bf16 map (channel, token, head, batch) of a view, 128-byte swizzle,
+// boxes of 64 channels x `rows` tokens; elements outside read as zero.
+static bool map_view(CUtensorMap* m, const View4& v, const Extent4& e, uint32_t rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(e.d), static_cast<cuuint64_t>(e.T), static_cast<cuuint64_t>(e.H),
+                        static_cast<cuuint64_t>(e.B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(v.st) * 2, static_cast<cuuint64_t>(v.sh) * 2,
+                           static_cast<cuuint64_t>(v.sb) * 2};
+  cuuint32_t box[4] = {64, rows, 1, 1}, es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP>
+static cudaError_t wattn_fwd_bf16(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
+  using C = WattnCfg<DP>;
+  static_assert(C::kSmem * C::kCtas <= kMaxSmemPerBlock, "dynamic shared memory above the SM's limit");
+  static bool done[64] = {};
+  const cudaError_t e = set_smem(k_wattn_fwd<DP>, C::kSmem, done);
+  if (e != cudaSuccess) return e;
+  WattnFwdParams f;
+  std::memset(&f, 0, sizeof(f));
+  const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
+  if (!map_view(&f.tmQ, a.q, eq, 128) || !map_view(&f.tmK, a.k, ek, 128) || !map_view(&f.tmV, a.v, ek, C::kVKeys))
+    return cudaErrorInvalidValue;
+  f.a = a;
+  f.nb = static_cast<int>(cdiv(D.Tq, 128));
+  const int64_t tiles = D.B * D.H * f.nb;
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  f.ntiles = static_cast<int>(tiles);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tiles, sm_count() * C::kCtas)));
+  return launch_pdl(k_wattn_fwd<DP>, grid, dim3(C::kThreads), C::kSmem, st, f);
+}
+
 template <int DP>
 static cudaError_t wattn_fwd_f32(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
   static bool done[64] = {};
@@ -243,12 +282,39 @@ static cudaError_t wattn_dkv_f32(const WattnDims& D, const WattnParams& a, cudaS
   return launch_pdl(k_wattn_dkv_f32<DP>, grid, dim3(kSimtThreads), SimtCfg<DP>::kBwdSmem, st, a, D.sink_tiles, D.parts);
 }
 
-#define LACT_BY_DP(DPV, CALL)                  \
+template <int DP, int MODE>
+static cudaError_t wattn_bwd_bf16(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
+  using C = BwdCfg<DP, MODE>;
+  static_assert(C::kSmem <= kMaxSmemPerBlock, "dynamic shared memory above the per-CTA limit");
+  static bool done[64] = {};
+  const cudaError_t e = set_smem(k_wattn_bwd<DP, MODE>, C::kSmem, done);
+  if (e != cudaSuccess) return e;
+  WattnBwdParams f;
+  std::memset(&f, 0, sizeof(f));
+  const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
+  const uint32_t rq = MODE == WATTN_DQ ? 128 : 64, rk = MODE == WATTN_DQ ? 64 : 128;
+  CUtensorMap *q = MODE == WATTN_DQ ? &f.tmA1 : &f.tmB1, *g = MODE == WATTN_DQ ? &f.tmA2 : &f.tmB2;
+  CUtensorMap *k = MODE == WATTN_DQ ? &f.tmB1 : &f.tmA1, *v = MODE == WATTN_DQ ? &f.tmB2 : &f.tmA2;
+  if (!map_view(q, a.q, eq, rq) || !map_view(g, a.dout, eq, rq) || !map_view(k, a.k, ek, rk) ||
+      !map_view(v, a.v, ek, rk))
+    return cudaErrorInvalidValue;
+  f.a = a;
+  f.sink_tiles = D.sink_tiles;
+  f.parts = D.parts;
+  f.per_head = MODE == WATTN_DQ ? static_cast<int>(cdiv(D.Tq, 128)) : D.sink_tiles * (D.parts - 1) + D.key_tiles;
+  const int64_t items = D.B * (MODE == WATTN_DQ ? D.H : D.Hkv) * f.per_head;
+  if (items > INT32_MAX) return cudaErrorInvalidValue;
+  f.nitems = static_cast<int>(items);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, sm_count())));
+  return launch_pdl(k_wattn_bwd<DP, MODE>, grid, dim3(C::kThreads), C::kSmem, st, f);
+}
+
+#define LACT_BY_DP(DPV, ...)                  \
   switch (DPV) {                               \
-    case 64: { constexpr int DP = 64; return CALL; }   \
-    case 128: { constexpr int DP = 128; return CALL; } \
-    case 192: { constexpr int DP = 192; return CALL; } \
-    default: { constexpr int DP = 256; return CALL; }  \
+    case 64: { constexpr int DP = 64; return __VA_ARGS__; }   \
+    case 128: { constexpr int DP = 128; return __VA_ARGS__; } \
+    case 192: { constexpr int DP = 192; return __VA_ARGS__; } \
+    default: { constexpr int DP = 256; return __VA_ARGS__; }  \
   }
 
 static cudaError_t launch_wattn_delta(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
@@ -267,14 +333,23 @@ static cudaError_t launch_wattn_sums(const WattnDims& D, const WattnParams& a, c
 
 static void wattn_fwd_run(const WattnDims& D, const WattnParams& a, cudaStream_t st, Launcher& L) {
   L.st = st;
-  L(K_WATTN_FWD, [&]() -> cudaError_t { LACT_BY_DP(D.DP, wattn_fwd_f32<DP>(D, a, st)) });
+  L(K_WATTN_FWD, [&]() -> cudaError_t {
+    LACT_BY_DP(D.DP, D.dtype == LACT_F32 ? wattn_fwd_f32<DP>(D, a, st) : wattn_fwd_bf16<DP>(D, a, st))
+  });
 }
 
 static void wattn_bwd_run(const WattnDims& D, const WattnParams& a, cudaStream_t st, Launcher& L) {
   L.st = st;
   L(K_WATTN_ELEM, [&] { return launch_wattn_delta(D, a, st); });
-  L(K_WATTN_DQ, [&]() -> cudaError_t { LACT_BY_DP(D.DP, wattn_dq_f32<DP>(D, a, st)) });
-  L(K_WATTN_DKV, [&]() -> cudaError_t { LACT_BY_DP(D.DP, wattn_dkv_f32<DP>(D, a, st)) });
+  L(K_WATTN_DQ, [&]() -> cudaError_t {
+    LACT_BY_DP(D.DP, D.dtype == LACT_F32 ? wattn_dq_f32<DP>(D, a, st) : (wattn_bwd_bf16<DP, WATTN_DQ>(D, a, st)))
+  });
+  if (D.dtype == LACT_F32) {
+    L(K_WATTN_DKV, [&]() -> cudaError_t { LACT_BY_DP(D.DP, wattn_dkv_f32<DP>(D, a, st)) });
+  } else {
+    L(K_WATTN_DKV, [&]() -> cudaError_t { LACT_BY_DP(D.DP, (wattn_bwd_bf16<DP, WATTN_DK>(D, a, st))) });
+    L(K_WATTN_DKV, [&]() -> cudaError_t { LACT_BY_DP(D.DP, (wattn_bwd_bf16<DP, WATTN_DV>(D, a, st))) });
+  }
   if (D.sink_tiles > 0) L(K_WATTN_ELEM, [&] { return launch_wattn_sums(D, a, st); });
 }
 
@@ -283,7 +358,8 @@ static int decode_validate(const lact_swa_sink_problem* p) {
   if (!p || p->B < 1 || p->H < 1 || p->Hkv < 1 || p->d < 1) return LACT_EINVAL;
   if (p->dtype != LACT_F32 && p->dtype != LACT_BF16) return LACT_EINVAL;
   if (p->H % p->Hkv != 0 || p->d % 8 != 0 || p->d > 256) return LACT_EINVAL;
-  if (p->window < 1 || p->sinks < 0 || !std::isfinite(p->scale)) return LACT_EINVAL;
+  if (p->window < 1 || p->sinks < 0 || !std::isfinite(p->scale) || !(p->scale > 0.f))
+    return LACT_EINVAL;
   if (p->window > (int64_t(1) << 30) || p->sinks > (int64_t(1) << 30)) return LACT_EINVAL;
   if (p->B * p->H > 65535) return LACT_EINVAL;
   return LACT_OK;
@@ -445,7 +521,6 @@ int lact_swa_sink_fwd(const lact_swa_sink_problem* p, const lact_tensor4* q, con
   WattnDims D;
   const int rc = wattn_validate(p, D);
   if (rc != LACT_OK) return rc;
-  if (D.dtype == LACT_BF16) return LACT_EINVAL;   // no kernel yet
   const int esz = D.dtype == LACT_BF16 ? 2 : 4;
   const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
   if (!view_ok(q, eq, esz) || !view_ok(k, ek, esz) || !view_ok(v, ek, esz) || !view_ok(out, eq, esz)) return LACT_EINVAL;
@@ -477,7 +552,6 @@ int lact_swa_sink_bwd(const lact_swa_sink_problem* p, const lact_tensor4* q, con
   WattnDims D;
   const int rc = wattn_validate(p, D);
   if (rc != LACT_OK) return rc;
-  if (D.dtype == LACT_BF16) return LACT_EINVAL;   // no kernel yet
   const int esz = D.dtype == LACT_BF16 ? 2 : 4;
   const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
   const lact_tensor4* qs[] = {q, out, dout, dq};

@@ -440,7 +440,7 @@ int lact_rotary_bwd(const lact_rotary_problem* p, const lact_tensor4* dq_out, co
  * >= 1 and sinks >= 0. */
 typedef struct lact_swa_sink_problem {
   int64_t B, H, Hkv, T, Tq, d, window, sinks;
-  float scale;      /* of the scores, usually 1 / sqrt(d) */
+  float scale;      /* of the scores, above 0, usually 1 / sqrt(d) */
   int32_t dtype;
 } lact_swa_sink_problem;
 

@@ -88,7 +88,7 @@ def test_rotary_arguments_refused():
 
 @pytest.mark.parametrize("bad", [
     dict(B=0), dict(H=0), dict(Hkv=0), dict(H=3), dict(T=0), dict(Tq=0), dict(Tq=65), dict(d=0), dict(d=60),
-    dict(d=264), dict(window=0), dict(sinks=-1), dict(scale=math.inf), dict(dtype=3), dict(B=20000),
+    dict(d=264), dict(window=0), dict(sinks=-1), dict(scale=math.inf), dict(scale=0.0), dict(scale=-1.0), dict(dtype=3), dict(B=20000),
     dict(T=(1 << 24) + 1),
 ])
 def test_attention_problems_refused(bad):

@@ -78,7 +78,7 @@ def test_cache_fill(T, window, sinks, dtype):
             assert torch.equal(c, want)
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_prompt_then_tokens_is_the_whole_sequence(dtype):
     """A prompt through rotary, attention and the cache, then token by token
     through rotary and the single-token form: the outputs of the attention over

@@ -84,7 +84,7 @@ CASES = [
 ]
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("B,H,Hkv,T,Tq,d,window,sinks,lengths,layout", CASES)
 def test_forward_and_backward(B, H, Hkv, T, Tq, d, window, sinks, lengths, layout, dtype):
     q, k, v, dout = make(B, H, Hkv, T, Tq, d, dtype, layout, seed=T + d)
@@ -98,7 +98,7 @@ def test_forward_and_backward(B, H, Hkv, T, Tq, d, window, sinks, lengths, layou
     check_backward(res, w, dtype, d, T * (H // Hkv))
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_padding_is_never_used(dtype):
     """NaN and infinities behind the lengths, in every input: rows there get
     out 0, lse -inf and gradients 0, the others are what they are without."""
@@ -124,7 +124,7 @@ def test_padding_is_never_used(dtype):
     assert ct.status() == ct.LACT_OK
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_large_scores(dtype):
     """Scores in the hundreds that rise along the keys, so the running maximum grows tile after tile."""
     B, H, T, d, window = 1, 1, 700, 64, 600
@@ -137,7 +137,7 @@ def test_large_scores(dtype):
     check_backward(ct.swa_sink_bwd(q, k, v, out, lse, dout, window, 2), w, dtype, d, T)
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_scale_outputs_and_repeats(dtype):
     """An own scale, outputs in a [B, T, H, d] layout, a workspace with other
     contents: the same bits each time, nothing written beside the outputs."""
@@ -180,3 +180,12 @@ def test_backward_is_the_forwards_gradient():
         noise = 2.0 ** -20 * float((out.double() * dout.double()).abs().sum()) / h
         assert abs(diff - want) <= h * h * size + noise, (n, diff, want)
 
+
+def test_long_sequence_far_sinks():
+    """The sinks' gradients over many far parts, bf16, on one head."""
+    T, d, window, sinks = 9000, 64, 128, 4
+    q, k, v, dout = make(1, 1, 1, T, T, d, BF16)
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks)
+    w = ao.attention(q, k, v, window, sinks, dout=dout)
+    check_forward(out, lse, w, BF16, d, window + sinks)
+    check_backward(ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks), w, BF16, d, T)

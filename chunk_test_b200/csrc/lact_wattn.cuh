@@ -85,8 +85,7 @@ static cudaError_t set_smem(F* kernel, int bytes, bool (&done)[64], bool big_clu
 
 // ------------------------------------------------------------------ rotary
 struct RotaryDims {
-  int64_t tiles;
-  int tile, pairs, vec, heads_per_block, smem;
+  int vec, units, rot_units, rows, head_blocks, per_block, ranges, smem;
 };
 
 static int rotary_validate(const lact_rotary_problem* p) {
@@ -99,45 +98,39 @@ static int rotary_validate(const lact_rotary_problem* p) {
   return LACT_OK;
 }
 
-// Vectors of 16 bytes where both halves of a pair start on one; tiles of 64
-// tokens (less where their angles would pass 64 KB or the tokens would not
-// fill the machine); the heads are split over blocks while there are fewer
-// than two blocks per SM, so that a single token's heads run at once.
+// Vectors of 4 channels where both halves of a pair start on one (interleaved
+// pairs: of 16 bytes), else single channels.  A block takes as many heads as 384 threads (512 where a head alone
+// has more units) hold, so angles are formed once for all of them.
 static RotaryDims rotary_dims(const lact_rotary_problem* p, bool sums) {
   RotaryDims r;
-  const int full = p->dtype == LACT_BF16 ? 8 : 4;
-  r.vec = p->interleaved || (p->rot / 2) % full == 0 ? full : 1;
-  const int step = p->interleaved ? full / 2 : r.vec;
-  r.pairs = static_cast<int>(rup(p->rot / 2, step));
-  const int64_t want = 2 * kPlanSMs;
-  int64_t tile = std::min<int64_t>(64, std::max<int64_t>(1, 8192 / r.pairs));
-  tile = std::min(tile, p->T);
-  while (tile > 16 && p->B * cdiv(p->T, tile) < want) tile /= 2;
-  r.tile = static_cast<int>(tile);
-  r.tiles = p->B * cdiv(p->T, tile);
+  const int d = static_cast<int>(p->d), rot = static_cast<int>(p->rot);
+  r.vec = p->interleaved ? (p->dtype == LACT_BF16 ? 8 : 4) : (rot / 2) % 4 == 0 ? 4 : 1;
+  r.rot_units = p->interleaved ? static_cast<int>(cdiv(rot, r.vec)) : rot / (2 * r.vec);
+  r.units = p->interleaved ? d / r.vec : r.rot_units + (d - rot) / r.vec;
   const int64_t heads = p->H + p->Hkv;
-  const int64_t groups = std::min(heads, std::max<int64_t>(1, cdiv(want, r.tiles)));
-  r.heads_per_block = static_cast<int>(cdiv(heads, groups));
-  const int threads = r.vec == 1 ? 512 : 256;
-  const int rot_units = p->interleaved ? 0 : static_cast<int>(p->rot / (2 * r.vec));
-  const int units = p->interleaved ? static_cast<int>(p->d) / r.vec
-                                   : rot_units + static_cast<int>(p->d - p->rot) / r.vec;
-  r.smem = r.tile * r.pairs * 8 + (sums ? threads / units * static_cast<int>(p->d) * 4 : 0);
+  const int64_t most = std::max<int64_t>(1, kRotaryThreads / r.units);
+  r.head_blocks = static_cast<int>(cdiv(heads, std::min(heads, most)));
+  // two blocks per SM: with sums one round of them, since each block writes its
+  // own; without, at most 32 tokens each, so that the last round is short
+  r.per_block = static_cast<int>(cdiv(p->B * p->T * r.head_blocks, 2 * kPlanSMs));
+  if (!sums) r.per_block = std::min(r.per_block, 2 * kRotaryTile);
+  r.per_block = static_cast<int>(std::min<int64_t>(std::max(r.per_block, 1), p->T));
+  r.ranges = static_cast<int>(cdiv(p->T, r.per_block));
+  r.rows = static_cast<int>(cdiv(heads, r.head_blocks));
+  r.smem = (kRotaryTile + 1) * r.rot_units * (p->interleaved ? r.vec / 2 : r.vec) * 8;
   return r;
 }
 
 static size_t rotary_bwd_workspace(const lact_rotary_problem* p) {
   const RotaryDims r = rotary_dims(p, true);
-  return static_cast<size_t>(rup(r.tiles * 2 * (p->H + p->Hkv) * p->d * 4, 256));
+  return static_cast<size_t>(rup(p->B * r.ranges * 2 * (p->H + p->Hkv) * p->d * 4, 256));
 }
 
 template <typename T, int V, bool INTER, bool BWD, bool AFF>
 static cudaError_t launch_rotary(const RotaryDims& r, const RotaryParams& a, cudaStream_t st) {
-  static bool done[64] = {};
-  const cudaError_t e = set_smem(k_rotary<T, V, INTER, BWD, AFF>, 160 * 1024, done);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(r.tiles), static_cast<unsigned>(cdiv(a.H + a.Hkv, r.heads_per_block)));
-  return launch_pdl(k_rotary<T, V, INTER, BWD, AFF>, grid, dim3(kRotaryThreads<V>), r.smem, st, a);
+  const dim3 grid(static_cast<unsigned>(a.B * r.ranges), static_cast<unsigned>(r.head_blocks));
+  return launch_pdl(k_rotary<T, V, INTER, BWD, AFF>, grid, dim3(static_cast<unsigned>(rup(r.units * r.rows, 32))),
+                    r.smem, st, a);
 }
 
 template <bool BWD, bool AFF>
@@ -146,7 +139,7 @@ static cudaError_t launch_rotary_any(const lact_rotary_problem* p, const RotaryD
   using B16 = __nv_bfloat16;
   if (p->dtype == LACT_BF16) {
     if (p->interleaved) return launch_rotary<B16, 8, true, BWD, AFF>(r, a, st);
-    return r.vec == 8 ? launch_rotary<B16, 8, false, BWD, AFF>(r, a, st)
+    return r.vec == 4 ? launch_rotary<B16, 4, false, BWD, AFF>(r, a, st)
                       : launch_rotary<B16, 1, false, BWD, AFF>(r, a, st);
   }
   if (p->interleaved) return launch_rotary<float, 4, true, BWD, AFF>(r, a, st);
@@ -160,8 +153,8 @@ static RotaryParams rotary_params(const lact_rotary_problem* p, const RotaryDims
   std::memset(&a, 0, sizeof(a));
   a.freqs = freqs; a.positions = positions; a.start = p->start; a.T = p->T;
   a.B = static_cast<int>(p->B); a.H = static_cast<int>(p->H); a.Hkv = static_cast<int>(p->Hkv);
-  a.d = static_cast<int>(p->d); a.rot = static_cast<int>(p->rot); a.pairs = r.pairs;
-  a.tile = r.tile; a.heads_per_block = r.heads_per_block; a.amp = p->amplitude;
+  a.d = static_cast<int>(p->d); a.rot = static_cast<int>(p->rot); a.units = r.units; a.rot_units = r.rot_units;
+  a.rows = r.rows; a.per_block = r.per_block; a.ranges = r.ranges; a.amp = p->amplitude;
   return a;
 }
 
@@ -508,7 +501,7 @@ int lact_rotary_bwd(const lact_rotary_problem* p, const lact_tensor4* dq_out, co
     L(K_ROTARY_SUMS, [&] {
       const int64_t n = 2 * (p->H + p->Hkv) * p->d;
       return launch_pdl(k_rotary_sums, dim3(static_cast<unsigned>(cdiv(n, 32))), dim3(512), 0, st,
-                        static_cast<const float*>(a.partial), static_cast<int>(r.tiles), a.H, a.Hkv, a.d, dq_scale,
+                        static_cast<const float*>(a.partial), static_cast<int>(p->B * r.ranges), a.H, a.Hkv, a.d, dq_scale,
                         dq_offset, dk_scale, dk_offset);
     });
   return L.err;

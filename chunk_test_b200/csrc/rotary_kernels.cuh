@@ -10,10 +10,12 @@
 // amp), dx = g * scale, dscale = sum_{b,t} g x, doffset = sum_{b,t} g.
 //
 // Bound by HBM: each element is read and written once (the backward of the
-// scales also reads x).  A block takes a tile of tokens and walks the heads,
-// so an angle is formed once and used by every head: p * freqs[i] in 64 bits,
-// because a position of 10^6 leaves a 32-bit product only 4 bits below the
-// turn, then the fraction of the turn goes to sincospif in 32.
+// scales also reads x).  A thread owns a few channels of one head and walks the
+// block's tokens, so scales, offsets and their gradients' sums stay in its
+// registers; the angles of a tile of tokens are formed once per block, in
+// shared memory, for all of its heads: p * freqs[i] in 64 bits, because a
+// position of 10^6 leaves a 32-bit product only 4 bits below the turn, then
+// the fraction of the turn goes to sincospif in 32.
 #pragma once
 
 #include "sm100.cuh"
@@ -26,9 +28,8 @@ struct View4 {
   int64_t sb, sh, st;
 };
 
-// 512 threads where a thread owns single channels (up to 511 units of a row)
-template <int V>
-constexpr int kRotaryThreads = V == 1 ? 512 : 256;
+constexpr int kRotaryThreads = 384;    // of a block, 512 where a thread owns single channels
+constexpr int kRotaryTile = 16;        // tokens whose angles are held at a time
 
 struct RotaryParams {
   View4 xq, xk;            // forward: inputs; backward: inputs, for the scales' gradients (else null)
@@ -37,11 +38,13 @@ struct RotaryParams {
   const double* freqs;     // [rot / 2], radians per position
   const int* positions;    // [B, T] or null: start + t
   const float *q_scale, *q_offset, *k_scale, *k_offset;   // [H, d], [Hkv, d] or null
-  float* partial;          // backward of the scales: [token tiles][2][H + Hkv][d]
+  float* partial;          // backward of the scales: [blocks][2][H + Hkv][d]
   int64_t start;
   int64_t T;
-  int B, H, Hkv, d, rot, pairs;   // pairs: rot / 2 rounded up to a whole vector
-  int tile, heads_per_block;      // tokens of a block, heads of a block
+  int B, H, Hkv, d, rot;
+  int units, rot_units;    // threads of a head; those that rotate
+  int rows;                // heads of a block
+  int per_block, ranges;   // tokens of a block, blocks of a sequence
   float amp;
 };
 
@@ -79,6 +82,8 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float* x) {
   if constexpr (V == 8)
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  else if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
   else *p = __float2bfloat16(x[0]);
 }
 template <int V>
@@ -91,161 +96,202 @@ __device__ __forceinline__ void load_params(const float* p, float* x) {
   }
 }
 
+// 16 or 8 bytes (V = 8 or 4) or one element (V = 1) as loaded
+template <typename T, int V>
+struct Raw {
+  uint4 w;
+  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    if constexpr (sizeof(T) == 4) {
+      x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
+      x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+    } else {
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(h[i] << 16);
+        x[2 * i + 1] = __uint_as_float(h[i] & 0xffff0000u);
+      }
+    }
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 4> {
+  uint2 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xffff0000u);
+    x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xffff0000u);
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T w;
+  __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ void get(float* x) const { x[0] = static_cast<float>(w); }
+};
+
 // A thread owns `V` channels at c0 and, for rotated units of the half layout,
 // the V partners at c0 + rot/2: both elements of every pair it touches, so the
-// output may be the input itself.  V is the 16-byte vector when rot/2 is a
-// multiple of it (interleaved pairs: always), else 1.
+// output may be the input itself.  V is 4 when rot/2 is a multiple of it, 16
+// bytes for interleaved pairs, else 1: eight bf16 channels a thread, whose
+// scales, offsets and sums leave room for two blocks of 12 warps an SM (16-byte
+// halves, 16 channels a thread, left 12 warps: 181 us where this takes 154, 5.2
+// TB/s, at B 2, 12 heads, T 32768, d 256; the rest goes to the angles, a
+// quarter of the instructions, between two barriers).  The backward of the
+// scales keeps 16 sums more and loads one token at a time (75 us where batches
+// of two spill and take 82, at T 8192).
+// Block (x, y): tokens [x % ranges * per_block, ..) of sequence x / ranges, heads
+// [y * rows, (y + 1) * rows); thread u + units * r: unit u of head y * rows + r.
 template <typename T, int V, bool INTER, bool BWD, bool AFF>
-__global__ void __launch_bounds__(kRotaryThreads<V>) k_rotary(const RotaryParams p) {
-  extern __shared__ float2 trig[];   // [tile][pairs] (amp cos, amp sin), then the sums' staging
+__global__ void __launch_bounds__(V == 1 ? 512 : kRotaryThreads, V == 1 ? 1 : 2) k_rotary(const RotaryParams p) {
+  // [kRotaryTile][pairs of a unit][rot_units]: (amp cos, amp sin), then the pairs' turns per position in that order
+  extern __shared__ float2 trig[];
   griddep_launch();
   griddep_wait();
   constexpr int kHalf = INTER ? 1 : 2;           // vectors of a rotated unit
-  constexpr int kThreads = kRotaryThreads<V>;
-  constexpr int kUnroll = V == 1 ? 2 : 4;
-  const int tiles = static_cast<int>((p.T + p.tile - 1) / p.tile);
-  const int b = blockIdx.x / tiles;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x % tiles) * p.tile;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(p.tile), p.T - t0));
-  for (int e = threadIdx.x; e < nt * p.pairs; e += kThreads) {
-    const int t = e / p.pairs, i = e % p.pairs;
-    float2 cs = make_float2(1.f, 0.f);           // pairs that pad the last vector pass through
-    if (2 * i < p.rot) {
-      const int64_t pos = p.positions ? p.positions[b * p.T + t0 + t] : p.start + t0 + t;
-      const double turns = static_cast<double>(pos) * p.freqs[i] * 0.15915494309189533577;   // 1 / (2 pi)
-      float s, c;
-      sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
-      cs = make_float2(p.amp * c, p.amp * (BWD ? -s : s));
-    }
-    trig[e] = cs;
-  }
-  __syncthreads();
-
-  const int rot_units = INTER ? (p.rot + V - 1) / V : p.rot / (2 * V);
-  const int units = INTER ? p.d / V : rot_units + (p.d - p.rot) / V;
-  const int rows = kThreads / units;
-  const int u = threadIdx.x % units, r = threadIdx.x / units;
-  const bool rotated = u < rot_units;
-  const int nvec = rotated ? kHalf : 1;
-  const int c0 = (INTER || rotated) ? u * V : p.rot + (u - rot_units) * V;
+  constexpr int kPairs = INTER ? V / 2 : V;      // pairs of a rotated unit
+  constexpr int kUnroll = AFF && BWD ? 1 : 4;    // tokens in flight
+  const int b = blockIdx.x / p.ranges;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x % p.ranges) * p.per_block;
+  const int ntok = static_cast<int>(min(static_cast<int64_t>(p.per_block), p.T - t0));
+  const int u = threadIdx.x % p.units, r = threadIdx.x / p.units;
+  const int hh = blockIdx.y * p.rows + r;
+  const bool active = r < p.rows && hh < p.H + p.Hkv, isq = hh < p.H;
+  const int h = isq ? hh : hh - p.H;
+  const bool rotated = u < p.rot_units;
+  const int nvec = active ? (rotated ? kHalf : 1) : 0;
+  const int c0 = (INTER || rotated) ? u * V : p.rot + (u - p.rot_units) * V;
   const int c1 = c0 + p.rot / 2;
-  const int pair0 = INTER ? c0 / 2 : c0;
-  const int h1 = min(static_cast<int>(blockIdx.y + 1) * p.heads_per_block, p.H + p.Hkv);
-  for (int hh = blockIdx.y * p.heads_per_block; hh < h1; ++hh) {
-    const bool isq = hh < p.H;
-    const int h = isq ? hh : hh - p.H;
-    const View4& xv = isq ? p.xq : p.xk;
-    const View4& yv = isq ? p.yq : p.yk;
-    const View4& dv = isq ? p.dq : p.dk;
-    // what is rotated and what is written
-    const View4& src = BWD ? yv : xv;
-    const View4& dst = BWD ? dv : yv;
-    const T* s0 = static_cast<const T*>(src.p) + b * src.sb + h * src.sh + t0 * src.st;
-    T* o0 = static_cast<T*>(dst.p) + b * dst.sb + h * dst.sh + t0 * dst.st;
-    const T* x0 = (BWD && AFF) ? static_cast<const T*>(xv.p) + b * xv.sb + h * xv.sh + t0 * xv.st : nullptr;
-    float sc[kHalf][V], of[kHalf][V], as[kHalf][V], ao[kHalf][V];
-    if constexpr (AFF) {
-      const float* sp = (isq ? p.q_scale : p.k_scale) + h * p.d;
-      const float* op = BWD ? nullptr : (isq ? p.q_offset : p.k_offset) + h * p.d;
+  const View4& xv = isq ? p.xq : p.xk;
+  const View4& yv = isq ? p.yq : p.yk;
+  const View4& dv = isq ? p.dq : p.dk;
+  // what is rotated and what is written
+  const View4& src = BWD ? yv : xv;
+  const View4& dst = BWD ? dv : yv;
+  const int64_t ss = src.st, ds = dst.st, xs = xv.st;
+  const T* s0 = static_cast<const T*>(src.p) + b * src.sb + h * src.sh + t0 * ss;
+  T* o0 = static_cast<T*>(dst.p) + b * dst.sb + h * dst.sh + t0 * ds;
+  const T* x0 = (BWD && AFF) ? static_cast<const T*>(xv.p) + b * xv.sb + h * xv.sh + t0 * xs : nullptr;
+  float sc[kHalf][V], of[kHalf][V], as[kHalf][V], ao[kHalf][V];
+  if constexpr (AFF) {
 #pragma unroll
-      for (int k = 0; k < kHalf; ++k) {
+    for (int k = 0; k < kHalf; ++k) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) as[k][i] = ao[k][i] = 0.f;
-        if (k < nvec) {
-          load_params<V>(sp + (k ? c1 : c0), sc[k]);
-          if constexpr (!BWD) load_params<V>(op + (k ? c1 : c0), of[k]);
-        }
+      for (int i = 0; i < V; ++i) as[k][i] = ao[k][i] = 0.f;
+      if (k < nvec) {
+        load_params<V>((isq ? p.q_scale : p.k_scale) + h * p.d + (k ? c1 : c0), sc[k]);
+        if constexpr (!BWD) load_params<V>((isq ? p.q_offset : p.k_offset) + h * p.d + (k ? c1 : c0), of[k]);
       }
     }
-    if (r < rows) {
-      for (int tb = r; tb < nt; tb += kUnroll * rows) {
-        float a[kUnroll][kHalf][V];
+  }
+  const int row_pairs = kPairs * p.rot_units;    // pairs past rot / 2 pad the last vector: angle 0
+  double* turns = reinterpret_cast<double*>(trig + kRotaryTile * row_pairs);
+  for (int x = threadIdx.x; x < row_pairs; x += blockDim.x) {
+    const int i = (x % p.rot_units) * kPairs + x / p.rot_units;
+    turns[x] = 2 * i < p.rot ? p.freqs[i] * 0.15915494309189533577 : nan("");   // 1 / (2 pi); a pad passes through
+  }
+  const int step_t = blockDim.x / row_pairs, step_x = blockDim.x % row_pairs;
+  const int first_t = threadIdx.x / row_pairs, first_x = threadIdx.x % row_pairs;
+  for (int base = 0; base < ntok; base += kRotaryTile) {
+    const int nt = min(kRotaryTile, ntok - base);
+    __syncthreads();
+    for (int t = first_t, x = first_x; t < nt;) {
+      const int64_t tok = t0 + base + t;
+      const int64_t pos = p.positions ? p.positions[b * p.T + tok] : p.start + tok;
+      const double n = static_cast<double>(pos) * turns[x];
+      float s, c;
+      sincospif(static_cast<float>(2.0 * (n - rint(n))), &s, &c);
+      const bool pad = INTER && isnan(n);
+      trig[t * row_pairs + x] = make_float2(pad ? 1.f : p.amp * c, pad ? 0.f : p.amp * (BWD ? -s : s));
+      t += step_t;
+      x += step_x;
+      if (x >= row_pairs) {
+        x -= row_pairs;
+        ++t;
+      }
+    }
+    __syncthreads();
+    if (nvec == 0) continue;
+    for (int tb = 0; tb < nt; tb += kUnroll) {
+      Raw<T, V> raw[kUnroll][kHalf], rx[kUnroll][kHalf];
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const int t = tb + j * rows;
-          if (t < nt) {
+      for (int j = 0; j < kUnroll; ++j)
+        if (tb + j < nt) {
+          const int64_t t = base + tb + j;
 #pragma unroll
-            for (int k = 0; k < kHalf; ++k)
-              if (k < nvec) load_vec<V>(s0 + t * src.st + (k ? c1 : c0), a[j][k]);
-          }
+          for (int k = 0; k < kHalf; ++k)
+            if (k < nvec) {
+              raw[j][k].load(s0 + t * ss + (k ? c1 : c0));
+              if constexpr (AFF && BWD) rx[j][k].load(x0 + t * xs + (k ? c1 : c0));
+            }
         }
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const int t = tb + j * rows;
-          if (t >= nt) break;
+      for (int j = 0; j < kUnroll; ++j) {
+        if (tb + j >= nt) break;
+        const int64_t t = base + tb + j;
+        float a[kHalf][V];
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) {
+          if (k < nvec) raw[j][k].get(a[k]);
           if constexpr (AFF && !BWD) {
 #pragma unroll
-            for (int k = 0; k < kHalf; ++k)
-#pragma unroll
-              for (int i = 0; i < V; ++i) a[j][k][i] = fmaf(a[j][k][i], sc[k][i], of[k][i]);
+            for (int i = 0; i < V; ++i) a[k][i] = fmaf(a[k][i], sc[k][i], of[k][i]);
           }
-          if (rotated) {
-            const float2* cs = trig + t * p.pairs + pair0;
-            if constexpr (INTER) {
+        }
+        if (rotated) {
+          const float2* cs = trig + (tb + j) * row_pairs + u;
 #pragma unroll
-              for (int i = 0; i < V; i += 2) {
-                const float2 w = cs[i / 2];
-                const float xa = a[j][0][i], xb = a[j][0][i + 1];
-                a[j][0][i] = xa * w.x - xb * w.y;
-                a[j][0][i + 1] = xb * w.x + xa * w.y;
-              }
-            } else {
+          for (int i = 0; i < kPairs; ++i) {
+            const float2 w = cs[i * p.rot_units];
+            float& xa = INTER ? a[0][2 * i] : a[0][i];
+            float& xb = INTER ? a[0][2 * i + 1] : a[kHalf - 1][i];
+            const float ya = xa * w.x - xb * w.y, yb = xb * w.x + xa * w.y;
+            xa = ya;
+            xb = yb;
+          }
+        }
+        if constexpr (AFF && BWD) {
+#pragma unroll
+          for (int k = 0; k < kHalf; ++k)
+            if (k < nvec) {
+              float x[V];
+              rx[j][k].get(x);
 #pragma unroll
               for (int i = 0; i < V; ++i) {
-                const float2 w = cs[i];
-                const float xa = a[j][0][i], xb = a[j][1][i];
-                a[j][0][i] = xa * w.x - xb * w.y;
-                a[j][1][i] = xb * w.x + xa * w.y;
+                as[k][i] = fmaf(a[k][i], x[i], as[k][i]);
+                ao[k][i] += a[k][i];
+                a[k][i] *= sc[k][i];
               }
             }
-          }
-          if constexpr (AFF && BWD) {
-#pragma unroll
-            for (int k = 0; k < kHalf; ++k)
-              if (k < nvec) {
-                float x[V];
-                load_vec<V>(x0 + t * xv.st + (k ? c1 : c0), x);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                  as[k][i] = fmaf(a[j][k][i], x[i], as[k][i]);
-                  ao[k][i] += a[j][k][i];
-                  a[j][k][i] *= sc[k][i];
-                }
-              }
-          }
-#pragma unroll
-          for (int k = 0; k < kHalf; ++k)
-            if (k < nvec) store_vec<V>(o0 + t * dst.st + (k ? c1 : c0), a[j][k]);
         }
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k)
+          if (k < nvec) store_vec<V>(o0 + t * ds + (k ? c1 : c0), a[k]);
       }
     }
-    if constexpr (AFF && BWD) {
-      // the block's sums over its tokens, in 32 bits and a fixed order: each
-      // thread's tokens, then the rows of threads
-      float* stage = reinterpret_cast<float*>(trig + p.tile * p.pairs);   // [rows][d]
-      for (int which = 0; which < 2; ++which) {
-        if (r < rows) {
+  }
+  if constexpr (AFF && BWD) {
+    // this block's sums, in 32 bits and in the tokens' order
 #pragma unroll
-          for (int k = 0; k < kHalf; ++k)
-            if (k < nvec)
+    for (int which = 0; which < 2; ++which) {
+      float* out = p.partial + ((static_cast<int64_t>(blockIdx.x) * 2 + which) * (p.H + p.Hkv) + hh) * p.d;
 #pragma unroll
-              for (int i = 0; i < V; ++i)
-                stage[r * p.d + (k ? c1 : c0) + i] = which ? ao[k][i] : as[k][i];
+      for (int k = 0; k < kHalf; ++k)
+        if (k < nvec) {
+          if constexpr (V >= 4) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) store_vec<4>(out + (k ? c1 : c0) + i, (which ? ao[k] : as[k]) + i);
+          } else {
+            out[k ? c1 : c0] = which ? ao[k][0] : as[k][0];
+          }
         }
-        __syncthreads();
-        for (int c = threadIdx.x; c < p.d; c += kThreads) {
-          float s = 0.f;
-          for (int k = 0; k < rows; ++k) s += stage[k * p.d + c];
-          p.partial[((static_cast<int64_t>(blockIdx.x) * 2 + which) * (p.H + p.Hkv) + hh) * p.d + c] = s;
-        }
-        __syncthreads();
-      }
     }
   }
 }
 
-// The scales' and offsets' gradients: the sum of the token tiles' partial sums
-// [tiles][2][H + Hkv][d], 32 columns a block, 16 interleaved chains per column
+// The scales' and offsets' gradients: the sum of the blocks' partial sums
+// [blocks][2][H + Hkv][d], 32 columns a block, 16 interleaved chains per column
 // joined in a fixed order.
 __global__ void __launch_bounds__(512) k_rotary_sums(const float* partial, int tiles, int H, int Hkv, int d,
                                                      float* dq_scale, float* dq_offset, float* dk_scale,

@@ -21,13 +21,15 @@ from ._abi import LactError
 _DT = {torch.float32: _abi.LACT_F32, torch.bfloat16: _abi.LACT_BF16}
 
 
-def _view(t):
-    s = t.stride()
-    return _abi.LactTensor4(t.data_ptr(), s[0], s[1], s[2])
+_T4, _byref = _abi.LactTensor4, ctypes.byref
 
 
 def _ref(t):
-    return None if t is None else ctypes.byref(_view(t))
+    """The tensor as a lact_tensor4 argument, or NULL."""
+    if t is None:
+        return None
+    s = t.stride()
+    return _byref(_T4(t.data_ptr(), s[0], s[1], s[2]))
 
 
 def _at(t):
@@ -36,17 +38,17 @@ def _at(t):
 
 def _tensor(name, t, shape, like):
     """A [B, heads, T, d] tensor of `like`'s dtype and device, channels contiguous."""
-    if t.device != like.device or t.dtype != like.dtype:
+    if t.dtype is not like.dtype or t.device != like.device:
         raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if shape[3] > 1 and t.stride(3) != 1:
+    if t.stride(3) != 1 and shape[3] > 1:
         raise ValueError(f"{name}'s channels must be contiguous")
     return t
 
 
 def _dense(name, t, shape, dtype, device):
-    if t.device != device or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
     return t
 
@@ -54,33 +56,24 @@ def _dense(name, t, shape, dtype, device):
 def _query(q):
     if q.dim() != 4:
         raise ValueError("q must be a [B, H, T, d] tensor")
-    if q.device.type != "cuda":
+    if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
     if q.dtype not in _DT:
         raise TypeError(f"unsupported dtype {q.dtype}")
-    return _tensor("q", q, q.shape, q)
+    if q.stride(3) != 1 and q.shape[3] > 1:
+        raise ValueError("q's channels must be contiguous")
 
 
-class _on:
-    """The call's device and stream: makes `device` current where another one is."""
-
-    def __init__(self, device, stream):
-        self.other = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
-        return ctypes.c_void_p(s.cuda_stream)
-
-    def __exit__(self, *a):
-        if self.other is not None:
-            self.other.__exit__(*a)
-        return False
-
-
-def _done(rc, name):
+def _call(name, device, stream, *args):
+    """The library's `name` on `device` (made current where another one is) and
+    its stream, torch's current one unless given."""
+    fn = getattr(_abi.lib(), name)
+    st = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if device.index == torch._C._cuda_getDevice():
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, st)
     if rc != _abi.LACT_OK:
         raise LactError(rc, name)
 
@@ -176,11 +169,9 @@ def rotary_fwd(q, k, freqs, *, positions=None, start=0, interleaved=False, ampli
         _tensor("out[0]", out[0], q.shape, q)
         if k is not None:
             _tensor("out[1]", out[1], k.shape, q)
-    with _on(q.device, stream) as st:
-        rc = _abi.lib().lact_rotary_fwd(
-            ctypes.byref(p), _ref(q), _ref(k), _at(freqs), _at(positions), _at(q_scale), _at(q_offset), _at(k_scale),
-            _at(k_offset), _ref(out[0]), _ref(None if k is None else out[1]), st)
-    _done(rc, "lact_rotary_fwd")
+    _call("lact_rotary_fwd", q.device, stream, _byref(p), _ref(q), _ref(k), _at(freqs), _at(positions),
+          _at(q_scale), _at(q_offset), _at(k_scale), _at(k_offset), _ref(out[0]), _ref(None if k is None else
+          out[1]))
     return out[0], (None if k is None else out[1])
 
 
@@ -212,17 +203,15 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
         if dk_out is not None:
             _tensor("k", k, dk_out.shape, dq_out)
             res["dk_scale"], res["dk_offset"] = torch.empty_like(k_scale), torch.empty_like(k_scale)
-        need = int(_abi.lib().lact_rotary_bwd_workspace_bytes(ctypes.byref(p)))
+        need = int(_abi.lib().lact_rotary_bwd_workspace_bytes(_byref(p)))
         if need == 0:
             raise LactError(_abi.LACT_EINVAL, "lact_rotary_bwd_workspace_bytes")
         workspace = _workspace(workspace, need, dq_out.device)
-    with _on(dq_out.device, stream) as st:
-        rc = _abi.lib().lact_rotary_bwd(
-            ctypes.byref(p), _ref(dq_out), _ref(dk_out), _at(freqs), _at(positions),
-            _ref(q) if affine else None, _ref(k) if affine and dk_out is not None else None, _at(q_scale),
-            _at(k_scale), _ref(res["dq"]), _ref(res["dk"]), _at(res["dq_scale"]), _at(res["dq_offset"]),
-            _at(res["dk_scale"]), _at(res["dk_offset"]), _at(workspace) if affine else None, need, st)
-    _done(rc, "lact_rotary_bwd")
+    _call("lact_rotary_bwd", dq_out.device, stream, _byref(p), _ref(dq_out), _ref(dk_out), _at(freqs),
+          _at(positions), _ref(q) if affine else None, _ref(k) if affine and dk_out is not None else None,
+          _at(q_scale), _at(k_scale), _ref(res["dq"]), _ref(res["dk"]), _at(res["dq_scale"]),
+          _at(res["dq_offset"]), _at(res["dk_scale"]), _at(res["dk_offset"]), _at(workspace) if affine else
+          None, need)
     return res
 
 
@@ -268,17 +257,15 @@ def swa_sink_fwd(q, k, v, window, sinks=0, *, lengths=None, scale=None, out=None
     if lse is None:
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     else:
-        _dense("lse", lse, tuple(q.shape[:3]), torch.float32, q.device)
-    with _on(q.device, stream) as st:
-        rc = _abi.lib().lact_swa_sink_fwd(ctypes.byref(p), _ref(q), _ref(k), _ref(v), _at(lengths), _ref(out),
-                                          _at(lse), st)
-    _done(rc, "lact_swa_sink_fwd")
+        _dense("lse", lse, q.shape[:3], torch.float32, q.device)
+    _call("lact_swa_sink_fwd", q.device, stream, _byref(p), _ref(q), _ref(k), _ref(v), _at(lengths),
+          _ref(out), _at(lse))
     return out, lse
 
 
 def swa_sink_bwd_workspace_bytes(q, k, window, sinks=0) -> int:
     p = _swa_sink_problem(q, k, window, sinks, None, k.shape[2], q.shape[2])
-    return int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(ctypes.byref(p)))
+    return int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(_byref(p)))
 
 
 def swa_sink_bwd(q, k, v, out, lse, dout, window, sinks=0, *, lengths=None, scale=None, dq=None, dk=None, dv=None,
@@ -291,19 +278,16 @@ def swa_sink_bwd(q, k, v, out, lse, dout, window, sinks=0, *, lengths=None, scal
     _keys(q, k, v, lengths)
     _tensor("out", out, q.shape, q)
     _tensor("dout", dout, q.shape, q)
-    _dense("lse", lse, tuple(q.shape[:3]), torch.float32, q.device)
+    _dense("lse", lse, q.shape[:3], torch.float32, q.device)
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else _tensor("dq", dq, q.shape, q)
     dk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dk is None else _tensor("dk", dk, k.shape, q)
     dv = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dv is None else _tensor("dv", dv, k.shape, q)
-    need = int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(ctypes.byref(p)))
+    need = int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(_byref(p)))
     if need == 0:
         raise LactError(_abi.LACT_EINVAL, "lact_swa_sink_bwd_workspace_bytes")
     workspace = _workspace(workspace, need, q.device)
-    with _on(q.device, stream) as st:
-        rc = _abi.lib().lact_swa_sink_bwd(ctypes.byref(p), _ref(q), _ref(k), _ref(v), _ref(out), _at(lse), _ref(dout),
-                                          _at(lengths), _ref(dq), _ref(dk), _ref(dv), _at(workspace),
-                                          workspace.numel(), st)
-    _done(rc, "lact_swa_sink_bwd")
+    _call("lact_swa_sink_bwd", q.device, stream, _byref(p), _ref(q), _ref(k), _ref(v), _ref(out), _at(lse),
+          _ref(dout), _at(lengths), _ref(dq), _ref(dk), _ref(dv), _at(workspace), workspace.numel())
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -334,10 +318,8 @@ def swa_sink_decode(q, k, v, k_cache, v_cache, seen, window, sinks=0, *, scale=N
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:
         _tensor("out", out, q.shape, q)
-    with _on(q.device, stream) as st:
-        rc = _abi.lib().lact_swa_sink_decode(ctypes.byref(p), _ref(q), _ref(k), _ref(v), _at(k_cache), _at(v_cache),
-                                             _at(seen), _ref(out), st)
-    _done(rc, "lact_swa_sink_decode")
+    _call("lact_swa_sink_decode", q.device, stream, _byref(p), _ref(q), _ref(k), _ref(v), _at(k_cache),
+          _at(v_cache), _at(seen), _ref(out))
     return out
 
 
@@ -350,7 +332,5 @@ def swa_cache_fill(k, v, k_cache, v_cache, window, sinks=0, *, lengths=None, str
     p = _swa_sink_problem(k, k, window, sinks, 1.0, T, 1)
     _keys(k, k, v, lengths)
     _caches(k, k, k_cache, v_cache, window, sinks)
-    with _on(k.device, stream) as st:
-        rc = _abi.lib().lact_swa_cache_fill(ctypes.byref(p), _ref(k), _ref(v), _at(lengths), _at(k_cache),
-                                            _at(v_cache), st)
-    _done(rc, "lact_swa_cache_fill")
+    _call("lact_swa_cache_fill", k.device, stream, _byref(p), _ref(k), _ref(v), _at(lengths), _at(k_cache),
+          _at(v_cache))

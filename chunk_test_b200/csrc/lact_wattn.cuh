@@ -237,7 +237,8 @@ static cudaError_t wattn_fwd_bf16(const WattnDims& D, const WattnParams& a, cuda
   WattnFwdParams f;
   std::memset(&f, 0, sizeof(f));
   const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
-  if (!map_view(&f.tmQ, a.q, eq, 128) || !map_view(&f.tmK, a.k, ek, 128) || !map_view(&f.tmV, a.v, ek, C::kVKeys))
+  if (!map_view(&f.tmQ, a.q, eq, 128) || !map_view(&f.tmK, a.k, ek, 128) || !map_view(&f.tmV, a.v, ek, C::kVKeys) ||
+      !map_view(&f.tmK32, a.k, ek, 32) || !map_view(&f.tmV32, a.v, ek, 32))
     return cudaErrorInvalidValue;
   f.a = a;
   f.nb = static_cast<int>(cdiv(D.Tq, 128));

@@ -2,24 +2,27 @@
 // Mask and formulas: wattn_common.cuh.
 //
 // A tile is 128 queries of one head; it walks the key tiles (128 keys) of the
-// sinks and of its window with an online softmax.  Roles of a CTA:
-//   warp 0     TMA producer of the queries and keys: a key slot is 128 keys x
-//              64 channels (16 KB), freed as soon as its part of S is done.
-//              (NS = 1: of the values too.)
-//   warp 1     issues S_j = Q K_j^T and O += P_j V_j (tcgen05, M = 128).
+// sinks and of its window with an online softmax.  Where the sinks end with at
+// most 32 keys of a tile, that tile is 32 keys wide in every step.  Roles:
+//   warp 0     TMA producer of the queries and keys (NS = 1: of the values too).
+//   warp 1     issues S_j = Q K_j^T (tcgen05, M = 128); NS = 1: and O += P_j V_j.
 //   warps 2-5  softmax, one query row per thread; P_j goes back to TMEM in
 //              bf16, over S_j, and is the second product's A operand from
 //              there, so shared memory carries K, V and Q only.
-//   warp 6     (NS = 2) TMA producer of the values, in slots of 64 keys x all
-//              channels (128 keys at d = 64).
+//   warp 6     (NS = 2) TMA producer of the values, in slots of 64 keys.
+//   warp 7     (NS = 2) issues O += P_j V_j.
+// One thread issues, and it waits and commits as little as the rings allow:
+// each costs 50 to 100 clocks in which it feeds nothing.
 // Head dims up to 128: two CTAs per SM with one score buffer each (NS = 1); one
 // CTA's products run under the other's exponentials.  Above: one CTA per SM
-// and two score buffers (NS = 2), S_{j+1} issued before P_j is ready.
+// and two score buffers (NS = 2).
 //
 // Bound by the exponentials (16 per clock and SM: 1024 clocks a tile of 128 x
 // 128, as many as both products at d = 128) up to d = 128, by the tensor pipe
 // (2048 clocks a tile at d = 256) above.
 #pragma once
+
+#include <type_traits>
 
 #include "swa_flash.cuh"
 #include "wattn_common.cuh"
@@ -60,18 +63,61 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
 }
 
+// 32 lanes x 32 columns; thread t of the warp gets lane 32 (warp % 4) + t.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Shared-memory descriptors of one operand differ by their start address only.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
 struct WattnFwdParams {
-  CUtensorMap tmQ;    // [d, Tq, H, B], box {64, 128}
-  CUtensorMap tmK;    // [d, T, Hkv, B], box {64, 128}
-  CUtensorMap tmV;    // [d, T, Hkv, B], box {64, kVKeys}
+  CUtensorMap tmQ;          // [d, Tq, H, B], box {64, 128}
+  CUtensorMap tmK, tmV;     // [d, T, Hkv, B], boxes {64, 128}, {64, kVKeys}
+  CUtensorMap tmK32, tmV32; // the same, box {64, 32}: a narrow sink tile
   WattnParams a;
-  int nb, ntiles;     // 128-query tiles per head, in all
+  int nb, ntiles;           // 128-query tiles per head, in all
 };
 
 // One query tile and the key tiles it walks: the sinks' before its window,
 // then its window's.
 struct QueryTile {
   int b, h, hk, q0, i0, len, sink_tiles, first, count;
+  int narrow;   // the sink tile of which at most 32 keys are sinks, or -1
   __device__ __forceinline__ QueryTile(const WattnParams& p, int nb, int tile) {
     const int bh = tile / nb;
     b = bh / p.H;
@@ -84,6 +130,7 @@ struct QueryTile {
     first = max(0, i0 - p.window + 1) >> 7;
     sink_tiles = min((p.sinks + 127) >> 7, first);
     count = i0 < len ? sink_tiles + (last >> 7) - first + 1 : 0;
+    narrow = sink_tiles > 0 && p.sinks - ((sink_tiles - 1) << 7) <= 32 ? sink_tiles - 1 : -1;
   }
   __device__ __forceinline__ int key0(int n) const { return (n < sink_tiles ? n : first + n - sink_tiles) << 7; }
 };
@@ -93,20 +140,18 @@ struct WattnCfg {
   static_assert(D % 64 == 0 && D >= 64 && D <= 256, "padded head dim");
   static constexpr int kNS = D <= 128 ? 1 : 2;            // score buffers
   static constexpr int kCtas = D <= 128 ? 2 : 1;          // CTAs per SM
-  static constexpr int kWarps = kNS == 1 ? 6 : 7;
-  static constexpr int kThreads = kWarps * 32;
-  static constexpr int kKb = D / 64;                      // key slots of a tile
-  static constexpr int kVKeys = D == 64 ? 128 : 64;
-  static constexpr int kVSlots = 128 / kVKeys;            // value slots of a tile
-  static constexpr int kVBox = kVKeys * 128;              // bytes of one box {64, kVKeys}
-  static constexpr int kKSlot = 16384, kVSlot = kKb * kVBox;
+  static constexpr int kThreads = kNS == 1 ? 192 : 256;
+  static constexpr int kKb = D / 64;
   static constexpr int kQBytes = kKb * 16384;
-  // slots of the two rings: 96 to 98 KB for one of two CTAs, 224 KB for a single one
-  static constexpr int kKR = D == 64 ? 3 : D == 128 ? 2 : D == 192 ? 5 : 4;
-  static constexpr int kVR = D <= 128 ? 2 : D == 192 ? 4 : 3;
+  // key slots of 128 keys x kKBlk 64-channel blocks, value slots of kVKeys keys
+  static constexpr int kKBlk = D == 256 ? 2 : kKb, kKPer = kKb / kKBlk;
+  static constexpr int kVKeys = kNS == 1 ? 128 : 64, kVPer = 128 / kVKeys;
+  static constexpr int kVBox = kVKeys * 128;              // bytes of one box {64, kVKeys}
+  static constexpr int kKSlot = kKBlk * 16384, kVSlot = kKb * kVBox;
+  static constexpr int kKR = D == 128 ? 1 : 2, kVR = D == 128 ? 1 : D == 64 ? 2 : 3;
   static constexpr int kOffK = kQBytes, kOffV = kOffK + kKR * kKSlot, kOffBar = kOffV + kVR * kVSlot;
-  // qfull qempty | kfull[] kempty[] | vfull[] vempty[] | sfull[NS] pfull[NS] | pvdone ofull oempty
-  static constexpr int kBars = 2 + 2 * kKR + 2 * kVR + 2 * kNS + 3;
+  // qfull qempty | kfull[] kempty[] | vfull[] vempty[] | sfull[NS] pfull[NS] pvdone[NS] | ofull oempty
+  static constexpr int kBars = 2 + 2 * kKR + 2 * kVR + 3 * kNS + 2;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
   static constexpr uint32_t kColO = 0, kColS = kNS == 1 ? 128 : 256, kCols = kNS == 1 ? 256 : 512;
 };
@@ -120,7 +165,8 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *qfull = bar, *qempty = bar + 1, *kfull = bar + 2, *kempty = kfull + KR, *vfull = kempty + KR,
-           *vempty = vfull + VR, *sfull = vempty + VR, *pfull = sfull + NS, *pvdone = pfull + NS, *ofull = pvdone + 1, *oempty = ofull + 1;
+           *vempty = vfull + VR, *sfull = vempty + VR, *pfull = sfull + NS, *pvdone = pfull + NS,
+           *ofull = pvdone + NS, *oempty = ofull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + C::kBars);
 
   griddep_launch();
@@ -140,8 +186,8 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
+      mbar_init(&pvdone[i], 1);
     }
-    mbar_init(pvdone, 1);
     mbar_init(ofull, 1);
     mbar_init(oempty, 4);
     fence_barrier_init();
@@ -159,7 +205,7 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
 
-  if (warp == 0 || (NS == 2 && warp == 6)) {
+  if (warp == 0 || warp == 6) {
     // ---------------------------------------------------------- producers
     if (lane == 0) {
       const bool keys = warp == 0, values = NS == 1 || warp == 6;
@@ -177,108 +223,110 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
         }
         for (int n = 0; ok && n < t.count; ++n) {
           const int j0 = t.key0(n);
-          for (int kb = 0; keys && ok && kb < C::kKb; ++kb, ++ik) {
+          const bool narrow = n == t.narrow;
+          for (int ks = 0; keys && ok && ks < C::kKPer; ++ks, ++ik) {
             const int s = ik % KR;
             if (ik >= KR && !mbar_wait(&kempty[s], ((ik / KR) - 1) & 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&kfull[s], C::kKSlot);
-            tma_load_4d(smem + C::kOffK + s * C::kKSlot, &p.tmK, &kfull[s], kb * 64, j0, t.hk, t.b);
+            mbar_arrive_expect_tx(&kfull[s], narrow ? C::kKSlot / 4 : C::kKSlot);
+            for (int kb = 0; kb < C::kKBlk; ++kb)
+              tma_load_4d(smem + C::kOffK + s * C::kKSlot + kb * 16384, narrow ? &p.tmK32 : &p.tmK, &kfull[s],
+                          (ks * C::kKBlk + kb) * 64, j0, t.hk, t.b);
           }
-          for (int vs = 0; values && ok && vs < C::kVSlots; ++vs, ++iv) {
+          for (int vs = 0; values && ok && vs < (narrow ? 1 : C::kVPer); ++vs, ++iv) {
             const int s = iv % VR;
             if (iv >= VR && !mbar_wait(&vempty[s], ((iv / VR) - 1) & 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&vfull[s], C::kVSlot);
+            mbar_arrive_expect_tx(&vfull[s], narrow ? C::kKb * 4096 : C::kVSlot);
             for (int nb = 0; nb < C::kKb; ++nb)
-              tma_load_4d(smem + C::kOffV + s * C::kVSlot + nb * C::kVBox, &p.tmV, &vfull[s], nb * 64,
-                          j0 + vs * C::kVKeys, t.hk, t.b);
+              tma_load_4d(smem + C::kOffV + s * C::kVSlot + nb * C::kVBox, narrow ? &p.tmV32 : &p.tmV, &vfull[s],
+                          nb * 64, j0 + vs * C::kVKeys, t.hk, t.b);
           }
         }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 7) {
     // ---------------------------------------------------------- products
-    constexpr uint32_t ids = idesc_bf16(128, 128, false, false), ido = idesc_bf16(128, D, false, true);
-    const uint32_t sbase = smem_u32(smem);
-    int ik = 0, iv = 0, sc = 0, pc = 0, tcq = 0, tco = 0;
-    // the next key tile whose scores are due
-    int qt = blockIdx.x, qn = 0, qcount = 0;
-    auto settle = [&]() {
-      while (qt < p.ntiles && (qcount = QueryTile(p.a, p.nb, qt).count) == 0) qt += gridDim.x;
-    };
-    auto scores = [&]() -> bool {
-      if (qn == 0 && !mbar_wait_warp(qfull, tcq & 1)) return false;
-      const uint32_t sd = tmem + C::kColS + (sc % NS) * 128;
-      for (int kb = 0; kb < C::kKb; ++kb, ++ik) {
-        const int s = ik % KR;
-        if (!mbar_wait_warp(&kfull[s], (ik / KR) & 1)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-          mma_kblock<false, false>(sd, sbase + kb * 16384, 0, sbase + C::kOffK + s * C::kKSlot, 0, ids, kb == 0);
+    if (lane == 0) {
+      const uint32_t sbase = smem_u32(smem);
+      const uint64_t qd = smem_desc_sw128(sbase, 16u, 1024u), kd = smem_desc_sw128(sbase + C::kOffK, 16u, 1024u),
+                     vd = smem_desc_sw128(sbase + C::kOffV, C::kVBox, 1024u);
+      constexpr uint32_t ids = idesc_bf16(128, 128, false, false), ids32 = idesc_bf16(128, 32, false, false),
+                         ido = idesc_bf16(128, D, false, true);
+      int ik = 0, iv = 0;
+      // S of the sc-th key tile in all; `n` counts from 0 in each query tile
+      auto scores = [&](int sc, bool narrow) -> bool {
+        const uint32_t sd = tmem + C::kColS + (sc % NS) * 128;
+        const uint32_t id = narrow ? ids32 : ids;
+        for (int ks = 0; ks < C::kKPer; ++ks, ++ik) {
+          const int s = ik % KR;
+          if (!mbar_wait(&kfull[s], (ik / KR) & 1)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kb = 0; kb < C::kKBlk; ++kb)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_bf16(sd, desc_at(qd, (ks * C::kKBlk + kb) * 16384 + k * 32),
+                        desc_at(kd, s * C::kKSlot + kb * 16384 + k * 32), id, (ks | kb | k) ? 1u : 0u);
           umma_commit(&kempty[s]);
         }
-        __syncwarp();
-      }
-      const bool end = qn + 1 == qcount;
-      if (lane == 0) {
         umma_commit(&sfull[sc % NS]);
-        if (end) umma_commit(qempty);
-      }
-      __syncwarp();
-      ++sc;
-      if (end) {
-        ++tcq;
-        qn = 0;
-        qt += gridDim.x;
-        settle();
-      } else {
-        ++qn;
-      }
-      return true;
-    };
-    settle();
-    bool ok = qt >= p.ntiles || scores();
-    for (int tile = blockIdx.x; ok && tile < p.ntiles; tile += gridDim.x) {
-      const QueryTile t(p.a, p.nb, tile);
-      if (t.count == 0) continue;
-      for (int n = 0; ok && n < t.count; ++n, ++pc) {
-        if (NS == 2 && qt < p.ntiles && !scores()) { ok = false; break; }
-        if (n == 0 && tco > 0 && !mbar_wait_warp(oempty, (tco - 1) & 1)) { ok = false; break; }
-        if (!mbar_wait_warp(&pfull[pc % NS], (pc / NS) & 1)) { ok = false; break; }
-        tc_fence_after();
+        return true;
+      };
+      auto output = [&](int pc, bool narrow, bool first, bool last) -> bool {
+        if (!mbar_wait(&pfull[pc % NS], (pc / NS) & 1)) return false;
         const uint32_t pa = tmem + C::kColS + (pc % NS) * 128;
-        const int j0 = t.key0(n);
-        for (int vs = 0; vs < C::kVSlots; ++vs, ++iv) {
+        for (int vs = 0; vs < (narrow ? 1 : C::kVPer); ++vs, ++iv) {
           const int s = iv % VR;
-          if (!mbar_wait_warp(&vfull[s], (iv / VR) & 1)) { ok = false; break; }
+          if (!mbar_wait(&vfull[s], (iv / VR) & 1)) return false;
           tc_fence_after();
-          const uint32_t vb = sbase + C::kOffV + s * C::kVSlot;
-          // rows behind the sequence: a probability of 0 times whatever is there must stay 0
-          const int keep = t.len - (j0 + vs * C::kVKeys);
-          if (keep < C::kVKeys) {
-            for (int e = max(keep, 0) * 8 + lane; e < C::kVKeys * 8; e += 32)
-              for (int nb = 0; nb < C::kKb; ++nb) st_shared_v4(vb + nb * C::kVBox + e * 16, 0, 0, 0, 0);
-            fence_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
 #pragma unroll
-            for (int k = 0; k < C::kVKeys / 16; ++k)
-              umma_bf16_ta(tmem + C::kColO, pa + (vs * C::kVKeys + k * 16) / 2,
-                           smem_desc_sw128(vb + k * 2048u, C::kVBox, 1024u), ido, (n == 0 && vs == 0 && k == 0) ? 0u : 1u);
-            umma_commit(&vempty[s]);
+          for (int k = 0; k < C::kVKeys / 16; ++k)
+            if (k < 2 || !narrow)
+              umma_bf16_ta(tmem + C::kColO, pa + (vs * C::kVKeys + k * 16) / 2, desc_at(vd, s * C::kVSlot + k * 2048),
+                           ido, (first && vs == 0 && k == 0) ? 0u : 1u);
+          umma_commit(&vempty[s]);
+        }
+        if (NS == 2) umma_commit(&pvdone[pc % NS]);
+        if (last) umma_commit(ofull);
+        return true;
+      };
+      int sc = 0, pc = 0, tc = 0;
+      bool ok = true;
+      if constexpr (NS == 2) {
+        for (int tile = blockIdx.x; ok && tile < p.ntiles; tile += gridDim.x) {
+          const QueryTile t(p.a, p.nb, tile);
+          if (t.count == 0) continue;
+          if (warp == 1) {
+            if (!mbar_wait(qfull, tc & 1)) break;
+            for (int n = 0; ok && n < t.count; ++n, ++sc) {
+              // P of two tiles ago, in this buffer, has been used
+              if (sc >= 2 && !mbar_wait(&pvdone[sc & 1], ((sc >> 1) - 1) & 1)) { ok = false; break; }
+              ok = scores(sc, n == t.narrow);
+            }
+            if (ok) umma_commit(qempty);
+          } else {
+            if (tc > 0 && !mbar_wait(oempty, (tc - 1) & 1)) break;
+            for (int n = 0; ok && n < t.count; ++n, ++pc) ok = output(pc, n == t.narrow, n == 0, n + 1 == t.count);
           }
-          __syncwarp();
+          ++tc;
         }
-        if (!ok) break;
-        if (lane == 0) {
-          umma_commit(pvdone);
-          if (n + 1 == t.count) umma_commit(ofull);
+      } else {
+        for (int tile = blockIdx.x; ok && tile < p.ntiles; tile += gridDim.x) {
+          const QueryTile t(p.a, p.nb, tile);
+          if (t.count == 0) continue;
+          if (!mbar_wait(qfull, tc & 1) || !scores(sc++, t.narrow == 0)) break;
+          if (t.count == 1) umma_commit(qempty);
+          for (int n = 0; ok && n < t.count; ++n, ++pc) {
+            if (n == 0 && tc > 0 && !mbar_wait(oempty, (tc - 1) & 1)) { ok = false; break; }
+            // S of the next tile goes over P: issued behind the product that reads it
+            ok = output(pc, n == t.narrow, n == 0, n + 1 == t.count) &&
+                 (n + 1 == t.count || scores(sc++, n + 1 == t.narrow));
+            if (ok && n + 2 == t.count) umma_commit(qempty);
+          }
+          ++tc;
         }
-        __syncwarp();
-        if (NS == 1 && qt < p.ntiles && !scores()) ok = false;
       }
-      ++tco;
     }
-  } else if (warp < 6) {
+  } else {
     // ---------------------------------------------------------- softmax
     // The reference maximum of a row is raised only when a tile's maximum is
     // above it by more than 8 in log2 units; the output row in TMEM is
@@ -288,84 +336,110 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
     const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float c2 = p.a.scale * 1.4426950408889634f;
     const int window = p.a.window, sinks = p.a.sinks;
-    int sc = 0, tc = 0;
+    int sc = 0, iv = 0, tc = 0;
     bool ok = true;
+    float mx, sum;
+    // one key tile of N columns; false where a wait gave up
+    auto step = [&](const QueryTile& t, int n, auto cols) -> bool {
+      constexpr int N = decltype(cols)::value;
+      const int sb = sc % NS, j0 = t.key0(n), i = t.i0 + r, last = t.i0 + 127;
+      if (!mbar_wait_warp(&sfull[sb], (sc / NS) & 1)) return false;
+      tc_fence_after();
+      const uint32_t ts = tq + C::kColS + sb * 128;
+      float sv[N];
+#pragma unroll
+      for (int c0 = 0; c0 < N; c0 += 32) tmem_ld32(ts + c0, sv + c0);
+      tmem_ld_wait();
+      const bool whole = j0 + N - 1 <= t.i0 && (j0 > last - window || j0 + N - 1 < sinks) && last < t.len;
+      if (!whole) {
+        const int hi = i < t.len ? i - j0 : -1, lo = i - window - j0, sk = sinks - j0;
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+          if (c > hi || (c <= lo && c >= sk)) sv[c] = -INFINITY;
+      }
+      float b4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+      for (int c = 4; c < N; c += 8) {
+        b4[0] = max3(b4[0], sv[c], sv[c + 1]);
+        b4[1] = max3(b4[1], sv[c + 2], sv[c + 3]);
+        if (c + 4 < N) {
+          b4[2] = max3(b4[2], sv[c + 4], sv[c + 5]);
+          b4[3] = max3(b4[3], sv[c + 6], sv[c + 7]);
+        }
+      }
+      const float bm = fmaxf(max3(b4[0], b4[1], b4[2]), b4[3]);
+      float fix = 1.0f;
+      bool grow = false;
+      if (mx == -INFINITY) {
+        mx = bm;   // no earlier key of this row: its output row and sum are zero
+      } else if ((bm - mx) * c2 > 8.0f) {
+        grow = true;
+        fix = ex2_approx((mx - bm) * c2);
+        mx = bm;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        // NS = 1: S_n came behind the last product; NS = 2: wait for it
+        if (NS == 2 && !mbar_wait_warp(&pvdone[(sc - 1) & 1], ((sc - 1) >> 1) & 1)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          float o[16];
+          __syncwarp();
+          tmem_ld16(tq + C::kColO + c0, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) o[c] *= fix;
+          tmem_st16(tq + C::kColO + c0, o);
+        }
+        sum *= fix;
+      }
+      const float off = mx == -INFINITY ? 0.f : -mx * c2;
+      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c0 = 0; c0 < N; c0 += 32) {
+        uint32_t hw[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float2 e = fma_f32x2(make_float2(sv[c0 + 2 * c], sv[c0 + 2 * c + 1]), make_float2(c2, c2),
+                               make_float2(off, off));
+          e.x = ex2_approx(e.x);
+          e.y = ex2_approx(e.y);
+          ps[c & 1] = add_f32x2(ps[c & 1], e);
+          hw[c] = pack_bf16x2(e.x, e.y);   // the second product's operand: half a step, 2^-8 of each
+        }
+        tmem_st16u(ts + c0 / 2, hw);
+      }
+      sum += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+      // value rows behind the sequence: a probability of 0 times whatever is there must stay 0
+      constexpr int per = N == 128 ? C::kVPer : 1, rows = N == 128 ? C::kVKeys : N;
+      if (t.len < j0 + N) {
+        for (int vs = 0; vs < per; ++vs) {
+          const int s = (iv + vs) % VR, keep = max(t.len - (j0 + vs * rows), 0);
+          if (!mbar_wait_warp(&vfull[s], ((iv + vs) / VR) & 1)) return false;
+          const uint32_t vb = smem_u32(smem) + C::kOffV + s * C::kVSlot;
+          for (int e = keep * 8 + r; e < rows * 8; e += 128)
+            for (int nb = 0; nb < C::kKb; ++nb) st_shared_v4(vb + nb * C::kVBox + e * 16, 0, 0, 0, 0);
+        }
+        fence_async_smem();
+      }
+      iv += per;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[sb]);
+      ++sc;
+      return true;
+    };
     for (int tile = blockIdx.x; ok && tile < p.ntiles; tile += gridDim.x) {
       const QueryTile t(p.a, p.nb, tile);
-      const int i = t.i0 + r, last = t.i0 + 127;
-      float mx = -INFINITY, sum = 0.f;
-      for (int n = 0; n < t.count; ++n, ++sc) {
-        const int sb = sc % NS, j0 = t.key0(n);
-        if (!mbar_wait_warp(&sfull[sb], (sc / NS) & 1)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t ts = tq + C::kColS + sb * 128;
-        float sv[128];
-#pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 16) tmem_ld16(ts + c0, sv + c0);
-        tmem_ld_wait();
-        const bool whole = j0 + 127 <= t.i0 && (j0 > last - window || j0 + 127 < sinks) && last < t.len;
-        if (!whole) {
-          const int hi = i < t.len ? i - j0 : -1, lo = i - window - j0, sk = sinks - j0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > hi || (c <= lo && c >= sk)) sv[c] = -INFINITY;
-        }
-        float b8[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) b8[c] = sv[c];
-#pragma unroll
-        for (int c = 8; c < 128; ++c) b8[c & 7] = fmaxf(b8[c & 7], sv[c]);
-        const float bm = fmaxf(fmaxf(fmaxf(b8[0], b8[1]), fmaxf(b8[2], b8[3])),
-                               fmaxf(fmaxf(b8[4], b8[5]), fmaxf(b8[6], b8[7])));
-        float fix = 1.0f;
-        bool grow = false;
-        if (mx == -INFINITY) {
-          mx = bm;   // no earlier key of this row: its output row and sum are zero
-        } else if ((bm - mx) * c2 > 8.0f) {
-          grow = true;
-          fix = ex2_approx((mx - bm) * c2);
-          mx = bm;
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-          // S_n was issued after P V of tile n - 2 (NS = 2) or n - 1 (NS = 1)
-          if (NS == 2 && !mbar_wait_warp(pvdone, (sc - 1) & 1)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            float o[16];
-            __syncwarp();
-            tmem_ld16(tq + C::kColO + c0, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] *= fix;
-            tmem_st16(tq + C::kColO + c0, o);
-          }
-          sum *= fix;
-        }
-        const float off = mx == -INFINITY ? 0.f : -mx * c2;
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t hw[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float e0 = ex2_approx(fmaf(sv[c0 + 2 * c], c2, off));
-            const float e1 = ex2_approx(fmaf(sv[c0 + 2 * c + 1], c2, off));
-            ps[c & 3] += e0 + e1;
-            hw[c] = pack_bf16x2(e0, e1);   // the second product's operand: half a step, 2^-8 of each
-          }
-          tmem_st16u(ts + c0 / 2, hw);
-        }
-        sum += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[sb]);
-      }
+      mx = -INFINITY;
+      sum = 0.f;
+      for (int n = 0; ok && n < t.count; ++n)
+        ok = n == t.narrow ? step(t, n, std::integral_constant<int, 32>()) : step(t, n, std::integral_constant<int, 128>());
       if (!ok) break;
       // out = O / sum, lse = the reference maximum + log sum
       const bool in = t.q0 + r < p.a.Tq;
-      const bool some = i < t.len;       // a token sees at least itself
+      const bool some = t.i0 + r < t.len;       // a token sees at least itself
       const float inv = some ? 1.0f / sum : 0.f;
       if (in)
         p.a.lse[(static_cast<int64_t>(t.b) * p.a.H + t.h) * p.a.Tq + t.q0 + r] =
@@ -384,8 +458,7 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
       for (int c0 = 0; c0 < D; c0 += 32) {
         float o[32];
         __syncwarp();
-        tmem_ld16(tq + C::kColO + c0, o);
-        tmem_ld16(tq + C::kColO + c0 + 16, o + 16);
+        tmem_ld32(tq + C::kColO + c0, o);
         tmem_ld_wait();
 #pragma unroll
         for (int g = 0; g < 4; ++g)

@@ -286,11 +286,10 @@ static cudaError_t wattn_bwd_bf16(const WattnDims& D, const WattnParams& a, cuda
   WattnBwdParams f;
   std::memset(&f, 0, sizeof(f));
   const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
-  const uint32_t rq = MODE == WATTN_DQ ? 128 : 64, rk = MODE == WATTN_DQ ? 64 : 128;
   CUtensorMap *q = MODE == WATTN_DQ ? &f.tmA1 : &f.tmB1, *g = MODE == WATTN_DQ ? &f.tmA2 : &f.tmB2;
   CUtensorMap *k = MODE == WATTN_DQ ? &f.tmB1 : &f.tmA1, *v = MODE == WATTN_DQ ? &f.tmB2 : &f.tmA2;
-  if (!map_view(q, a.q, eq, rq) || !map_view(g, a.dout, eq, rq) || !map_view(k, a.k, ek, rk) ||
-      !map_view(v, a.v, ek, rk))
+  if (!map_view(q, a.q, eq, 128) || !map_view(g, a.dout, eq, 128) || !map_view(k, a.k, ek, 128) ||
+      !map_view(v, a.v, ek, 128))
     return cudaErrorInvalidValue;
   f.a = a;
   f.sink_tiles = D.sink_tiles;

@@ -11,14 +11,19 @@
 // 512 + 256 columns of accumulators at d = 256, and TMEM has 512.
 //
 // Resident operands A1 (Q or K) and A2 (dout or V), 128 rows; streamed tiles
-// of 64 rows B1 (K or Q) and B2 (V or dout).  64 rows, because with A1 and A2
-// (128 KB at d = 256) only 96 KB are left for the stream.  Roles:
-//   warp 0     TMA producer.
-//   warp 1     issues S = A1 B1^T, dP = A2 B2^T into one of two TMEM buffers,
-//              and dX += dS B1 (dV: P B2) with dS in TMEM in bf16.
-//   warps 2-9  two groups of four, one per buffer; a thread owns one row.
-// Bound by the tensor pipe: an M 128, N 64 product reads 6 KB of shared memory
-// for 32 clocks of products and takes 48.
+// of 128 rows B1 (K or Q) and B2 (V or dout).  128, because a product of N = 64
+// takes as long as one of N = 128: both read the same 4 KB of A per 16 channels
+// (tiles of 64 rows measured 1589 us where this takes TIME_A at B 2, H 6, T 8192,
+// d 256, window 2048).  Roles:
+//   warp 0      TMA producer of A and B1.
+//   warp 10     TMA producer of B2.
+//   warp 1      issues S = A1 B1^T, dP = A2 B2^T and dX += dS B1 (dV: P B2),
+//               dS in TMEM in bf16 over S.  One thread, in the order
+//               S(n), dP(n+1) once dP(n) has been read, dX(n): the tensor pipe
+//               forms dP(n+1) while dS(n) is computed.
+//   warps 2-9   dS (dV: P): two threads per row, 64 columns each.
+// Bound by the tensor pipe; at d = 256 shared memory holds one B1 tile, so its
+// load is exposed in part.
 #pragma once
 
 #include "wattn_fwd.cuh"
@@ -28,21 +33,21 @@ namespace lact {
 enum WattnMode { WATTN_DQ, WATTN_DK, WATTN_DV };
 
 struct WattnBwdParams {
-  CUtensorMap tmA1, tmA2;   // box {64, 128}: q, dout (dQ) or k, v (dK, dV)
-  CUtensorMap tmB1, tmB2;   // box {64, 64}: k, v (dQ) or q, dout (dK, dV)
+  CUtensorMap tmA1, tmA2;   // q, dout (dQ) or k, v (dK, dV), box {64, 128}
+  CUtensorMap tmB1, tmB2;   // k, v (dQ) or q, dout (dK, dV), box {64, 128}
   WattnParams a;
   int nitems, per_head;     // items in all, and per (batch, head of A)
   int sink_tiles, parts;    // dK, dV: the split of the sink tiles (KeyPart)
 };
 
-// An item: 128 rows of A and the tiles of 64 rows of B that it walks.
+// An item: 128 rows of A and the tiles of 128 rows of B that it walks.
 template <int MODE>
 struct BwdItem {
   int b, ha, a0;            // batch, head and first row of A
   int pos;                  // position of A's first row
   int len, count;           // the sequence's length, tiles of B
   int hb0, per, lo, hi;     // dK, dV: first head of B, tiles per head, query positions [lo, hi)
-  int sink_tiles, first;    // dQ: tiles of 64 keys of the sinks, first of the window's
+  int sink_tiles, first;    // dQ: tiles of 128 keys of the sinks, first of the window's
   int kt, part;
   __device__ __forceinline__ BwdItem(const WattnBwdParams& q, int item) {
     const WattnParams& p = q.a;
@@ -55,9 +60,9 @@ struct BwdItem {
       pos = a0 + p.T - p.Tq;
       len = seq_len(p, b);
       const int last = min(min(pos + 128, p.T), len) - 1;
-      first = max(0, pos - p.window + 1) >> 6;
-      sink_tiles = min((p.sinks + 63) >> 6, first);
-      count = pos < len ? sink_tiles + (last >> 6) - first + 1 : 0;
+      first = max(0, pos - p.window + 1) >> 7;
+      sink_tiles = min((p.sinks + 127) >> 7, first);
+      count = pos < len ? sink_tiles + (last >> 7) - first + 1 : 0;
     } else {
       b = ba / p.Hkv;
       ha = ba % p.Hkv;
@@ -70,50 +75,53 @@ struct BwdItem {
       const KeyPart kp = key_part(kt, part, 128, p.window, p.T, p.far_rows);
       lo = max(kp.lo, p.T - p.Tq);
       hi = min(kp.hi, len);
-      per = hi > lo ? (hi - lo + 63) >> 6 : 0;
+      per = hi > lo ? (hi - lo + 127) >> 7 : 0;
       count = per * p.group;
     }
   }
   __device__ __forceinline__ int head(int n) const { return MODE == WATTN_DQ ? hb0 : hb0 + n / per; }
   // the position of B's first row
   __device__ __forceinline__ int at(int n) const {
-    if (MODE == WATTN_DQ) return (n < sink_tiles ? n : first + n - sink_tiles) << 6;
-    return lo + (n % per) * 64;
+    if (MODE == WATTN_DQ) return (n < sink_tiles ? n : first + n - sink_tiles) << 7;
+    return lo + (n % per) * 128;
   }
 };
 
 template <int D, int MODE>
 struct BwdCfg {
   static constexpr int kKb = D / 64;
+  static constexpr bool kDv = MODE == WATTN_DV;
   static constexpr int kABytes = kKb * 16384;
-  static constexpr int kAll = MODE == WATTN_DV ? kABytes : 2 * kABytes;
-  static constexpr int kBBytes = kKb * 8192;              // a tile of 64 rows
-  static constexpr int kTiles = (229376 - kAll) / kBBytes > 6 ? 6 : (229376 - kAll) / kBBytes;   // of both rings
-  // dV holds B2 until its product is done, the others B1
-  static constexpr int kR1 = MODE == WATTN_DV ? kTiles / 2 : (kTiles + 1) / 2;
-  static constexpr int kR2 = kTiles - kR1;
-  // B2 is a K-major operand in dQ and dK: its 64-channel blocks come and go singly
-  static constexpr int kS2 = MODE == WATTN_DV ? kR2 : kR2 * kKb;
-  static constexpr int kB2Slot = MODE == WATTN_DV ? kBBytes : 8192;
-  static constexpr int kOffB1 = kAll, kOffB2 = kOffB1 + kR1 * kBBytes, kOffCol = kOffB2 + kR2 * kBBytes;
-  static constexpr int kOffBar = kOffCol + 2 * 2 * 64 * 4;   // lse and delta of two tiles' columns
-  // afull aempty | b1full[] b1empty[] | b2full[] b2empty[] | sfull[2] pfull[2] cfull[2] | xfull xempty
-  static constexpr int kBars = 2 + 2 * kR1 + 2 * kS2 + 6 + 2;
+  static constexpr int kAll = kDv ? kABytes : 2 * kABytes;
+  static constexpr int kTile = kKb * 16384;                // a B tile of 128 rows
+  // The operand of the last product (B1; dV: B2) stays until that product is
+  // done: whole tiles.  The other one is K-major only and goes by blocks of 64
+  // channels.
+  static constexpr int kBlocks = (229376 - kAll) / 16384;  // 16 KB blocks there is room for
+  static constexpr int kRx = kBlocks >= 2 * kKb + 2 ? 2 : 1;
+  static constexpr int kRy0 = kBlocks - kRx * kKb, kRy = kRy0 > 2 * kKb ? 2 * kKb : kRy0;
+  static_assert(kRy >= 2, "room for two blocks");
+  static constexpr int kOffX = kAll, kOffY = kOffX + kRx * kTile, kOffCol = kOffY + kRy * 16384;
+  static constexpr int kOffBar = kOffCol + 2 * 128 * 4;    // lse and delta of a tile's columns
+  // afull aempty | xfull[] xempty[] | yfull[] yempty[] | sfull dfull pfull dread cfull | gfull gempty
+  // (dV: S and P have two buffers, sfull[2] and pfull[2])
+  static constexpr int kBars = 2 + 2 * kRx + 2 * kRy + 5 + 2;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
-  static constexpr int kThreads = 320;
-  static constexpr uint32_t kColX = 0, kColS = 256;          // buffers of 64 + 64 columns
+  static constexpr int kThreads = 352;
+  static constexpr uint32_t kColX = 0, kColS = 256, kColD = 384;
 };
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ WattnBwdParams p) {
+__global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ WattnBwdParams p) {
   using C = BwdCfg<D, MODE>;
-  constexpr int R1 = C::kR1, S2 = C::kS2;
+  constexpr int RX = C::kRx, RY = C::kRy, KB = C::kKb;
+  constexpr bool DV = C::kDv;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t *afull = bar, *aempty = bar + 1, *b1full = bar + 2, *b1empty = b1full + R1, *b2full = b1empty + R1,
-           *b2empty = b2full + S2, *sfull = b2empty + S2, *pfull = sfull + 2, *cfull = pfull + 2, *xfull = cfull + 2,
-           *xempty = xfull + 1;
+  uint64_t *afull = bar, *aempty = bar + 1, *xfull = bar + 2, *xempty = xfull + RX, *yfull = xempty + RX,
+           *yempty = yfull + RY, *sfull = yempty + RY, *dfull = sfull + 1, *pfull = dfull + 1, *dread = pfull + 1,
+           *cfull = dread + 1, *gfull = cfull + 1, *gempty = gfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + C::kBars);
 
   griddep_launch();
@@ -122,21 +130,21 @@ __global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ Wa
   if (threadIdx.x == 0) {
     mbar_init(afull, 1);
     mbar_init(aempty, 1);
-    for (int i = 0; i < R1; ++i) {
-      mbar_init(&b1full[i], 1);
-      mbar_init(&b1empty[i], 1);
+    for (int i = 0; i < RX; ++i) {
+      mbar_init(&xfull[i], 1);
+      mbar_init(&xempty[i], 1);
     }
-    for (int i = 0; i < S2; ++i) {
-      mbar_init(&b2full[i], 1);
-      mbar_init(&b2empty[i], 1);
+    for (int i = 0; i < RY; ++i) {
+      mbar_init(&yfull[i], 1);
+      mbar_init(&yempty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
-      mbar_init(&cfull[i], 4);
-    }
-    mbar_init(xfull, 1);
-    mbar_init(xempty, 8);
+    mbar_init(sfull, 1);
+    mbar_init(dfull, 1);
+    mbar_init(dread, 8);
+    mbar_init(pfull, 8);
+    mbar_init(cfull, 8);
+    mbar_init(gfull, 1);
+    mbar_init(gempty, 8);
     fence_barrier_init();
     tma_prefetch_map(&p.tmA1);
     tma_prefetch_map(&p.tmA2);
@@ -154,45 +162,41 @@ __global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ Wa
   griddep_wait();
   const int off = p.a.T - p.a.Tq;                     // position of query row 0
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
+  if (warp == 0 || warp == 10) {
+    // ---------------------------------------------------------- producers
+    // X: the operand of the last product, whole tiles; Y: the other one, by blocks
     if (lane == 0) {
-      int i1 = 0, i2 = 0, ic = 0;
+      const bool x = warp == 0;
+      const CUtensorMap* map = (x != DV) ? &p.tmB1 : &p.tmB2;
+      int ib = 0, ic = 0;
       bool ok = true;
       for (int item = blockIdx.x; ok && item < p.nitems; item += gridDim.x) {
         const BwdItem<MODE> t(p, item);
         if (t.count == 0) continue;
-        if (ic > 0 && !mbar_wait(aempty, (ic - 1) & 1)) break;
-        ++ic;
-        mbar_arrive_expect_tx(afull, C::kAll);
-        for (int kb = 0; kb < C::kKb; ++kb) {
-          tma_load_4d(smem + kb * 16384, &p.tmA1, afull, kb * 64, t.a0, t.ha, t.b);
-          if (MODE != WATTN_DV)
-            tma_load_4d(smem + C::kABytes + kb * 16384, &p.tmA2, afull, kb * 64, t.a0, t.ha, t.b);
+        if (x) {
+          if (ic > 0 && !mbar_wait(aempty, (ic - 1) & 1)) break;
+          ++ic;
+          mbar_arrive_expect_tx(afull, C::kAll);
+          for (int kb = 0; kb < KB; ++kb) {
+            tma_load_4d(smem + kb * 16384, &p.tmA1, afull, kb * 64, t.a0, t.ha, t.b);
+            if (!DV) tma_load_4d(smem + C::kABytes + kb * 16384, &p.tmA2, afull, kb * 64, t.a0, t.ha, t.b);
+          }
         }
         for (int n = 0; ok && n < t.count; ++n) {
           const int row = t.at(n) - (MODE == WATTN_DQ ? 0 : off), hb = t.head(n);
-          {
-            const int s = i1 % R1;
-            if (i1 >= R1 && !mbar_wait(&b1empty[s], ((i1 / R1) - 1) & 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&b1full[s], C::kBBytes);
-            for (int kb = 0; kb < C::kKb; ++kb)
-              tma_load_4d(smem + C::kOffB1 + s * C::kBBytes + kb * 8192, &p.tmB1, &b1full[s], kb * 64, row, hb, t.b);
-            ++i1;
-          }
-          if (MODE == WATTN_DV) {
-            const int s = i2 % S2;
-            if (i2 >= S2 && !mbar_wait(&b2empty[s], ((i2 / S2) - 1) & 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&b2full[s], C::kBBytes);
-            for (int kb = 0; kb < C::kKb; ++kb)
-              tma_load_4d(smem + C::kOffB2 + s * C::kBBytes + kb * 8192, &p.tmB2, &b2full[s], kb * 64, row, hb, t.b);
-            ++i2;
+          if (x) {
+            const int s = ib % RX;
+            if (ib >= RX && !mbar_wait(&xempty[s], ((ib / RX) - 1) & 1)) { ok = false; break; }
+            mbar_arrive_expect_tx(&xfull[s], C::kTile);
+            for (int kb = 0; kb < KB; ++kb)
+              tma_load_4d(smem + C::kOffX + s * C::kTile + kb * 16384, map, &xfull[s], kb * 64, row, hb, t.b);
+            ++ib;
           } else {
-            for (int kb = 0; kb < C::kKb; ++kb, ++i2) {
-              const int s = i2 % S2;
-              if (i2 >= S2 && !mbar_wait(&b2empty[s], ((i2 / S2) - 1) & 1)) { ok = false; break; }
-              mbar_arrive_expect_tx(&b2full[s], 8192);
-              tma_load_4d(smem + C::kOffB2 + s * 8192, &p.tmB2, &b2full[s], kb * 64, row, hb, t.b);
+            for (int kb = 0; kb < KB; ++kb, ++ib) {
+              const int s = ib % RY;
+              if (ib >= RY && !mbar_wait(&yempty[s], ((ib / RY) - 1) & 1)) { ok = false; break; }
+              mbar_arrive_expect_tx(&yfull[s], 16384);
+              tma_load_4d(smem + C::kOffY + s * 16384, map, &yfull[s], kb * 64, row, hb, t.b);
             }
           }
         }
@@ -200,107 +204,95 @@ __global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ Wa
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
-    constexpr uint32_t ids = idesc_bf16(128, 64, false, false), idx = idesc_bf16(128, D, false, true);
-    const uint32_t sbase = smem_u32(smem);
-    int i1 = 0, i2 = 0, sc = 0, pc = 0, ica = 0, icx = 0;
-    int nt = blockIdx.x, nn = 0, ncount = 0;          // the next tile whose scores are due
-    auto settle = [&]() {
-      while (nt < p.nitems && (ncount = BwdItem<MODE>(p, nt).count) == 0) nt += gridDim.x;
-    };
-    // rows of a 64-row tile at or past `keep` become zeros (64 channels x 128 B blocks)
-    auto clear = [&](uint32_t base, int keep) {
-      if (keep >= 64) return;
-      for (int e = max(keep, 0) * 8 + lane; e < 512; e += 32)
-        for (int kb = 0; kb < C::kKb; ++kb) st_shared_v4(base + kb * 8192 + e * 16, 0, 0, 0, 0);
-      fence_async_smem();
-      __syncwarp();
-    };
-    auto scores = [&]() -> bool {
-      const BwdItem<MODE> t(p, nt);
-      if (nn == 0 && !mbar_wait_warp(afull, ica & 1)) return false;
-      const uint32_t sd = tmem + C::kColS + (sc & 1) * 128;
-      const int s1 = i1 % R1;
-      if (!mbar_wait_warp(&b1full[s1], (i1 / R1) & 1)) return false;
-      tc_fence_after();
-      const uint32_t b1 = sbase + C::kOffB1 + s1 * C::kBBytes;
-      // rows behind the sequence: a dS of 0 times whatever is there must stay 0
-      if (MODE != WATTN_DV) clear(b1, t.len - t.at(nn));
-      if (lane == 0) {
-        for (int kb = 0; kb < C::kKb; ++kb)
-          mma_kblock<false, false>(sd, sbase + kb * 16384, 0, b1 + kb * 8192, 0, ids, kb == 0);
-        if (MODE == WATTN_DV) umma_commit(&b1empty[s1]);
-      }
-      __syncwarp();
-      ++i1;
-      if (MODE != WATTN_DV) {
-        for (int kb = 0; kb < C::kKb; ++kb, ++i2) {
-          const int s = i2 % S2;
-          if (!mbar_wait_warp(&b2full[s], (i2 / S2) & 1)) return false;
+    if (lane == 0) {
+      constexpr uint32_t ids = idesc_bf16(128, 128, false, false), idx = idesc_bf16(128, D, false, true);
+      const uint32_t sbase = smem_u32(smem);
+      const uint64_t a1 = smem_desc_sw128(sbase, 16u, 1024u), a2 = smem_desc_sw128(sbase + C::kABytes, 16u, 1024u),
+                     xk = smem_desc_sw128(sbase + C::kOffX, 16u, 1024u),
+                     xm = smem_desc_sw128(sbase + C::kOffX, 16384u, 1024u),
+                     yk = smem_desc_sw128(sbase + C::kOffY, 16u, 1024u);
+      int iy = 0;
+      // the product of a resident operand with the next tile of Y, by blocks
+      auto with_y = [&](uint32_t d, uint64_t a) -> bool {
+        for (int kb = 0; kb < KB; ++kb, ++iy) {
+          const int s = iy % RY;
+          if (!mbar_wait(&yfull[s], (iy / RY) & 1)) return false;
           tc_fence_after();
-          if (lane == 0) {
-            mma_kblock<false, false>(sd + 64, sbase + C::kABytes + kb * 16384, 0, sbase + C::kOffB2 + s * 8192, 0, ids,
-                                     kb == 0);
-            umma_commit(&b2empty[s]);
-          }
-          __syncwarp();
-        }
-      }
-      const bool end = nn + 1 == ncount;
-      if (lane == 0) {
-        umma_commit(&sfull[sc & 1]);
-        if (end) umma_commit(aempty);
-      }
-      __syncwarp();
-      ++sc;
-      if (end) {
-        ++ica;
-        nn = 0;
-        nt += gridDim.x;
-        settle();
-      } else {
-        ++nn;
-      }
-      return true;
-    };
-    settle();
-    bool ok = nt >= p.nitems || scores();
-    for (int item = blockIdx.x; ok && item < p.nitems; item += gridDim.x) {
-      const BwdItem<MODE> t(p, item);
-      if (t.count == 0) continue;
-      for (int n = 0; ok && n < t.count; ++n, ++pc) {
-        if (nt < p.nitems && !scores()) { ok = false; break; }
-        if (n == 0 && icx > 0 && !mbar_wait_warp(xempty, (icx - 1) & 1)) { ok = false; break; }
-        if (!mbar_wait_warp(&pfull[pc & 1], (pc >> 1) & 1)) { ok = false; break; }
-        const uint32_t pa = tmem + C::kColS + (pc & 1) * 128;
-        const int s = MODE == WATTN_DV ? pc % S2 : pc % R1;
-        const uint32_t xb = sbase + (MODE == WATTN_DV ? C::kOffB2 : C::kOffB1) + s * C::kBBytes;
-        if (MODE == WATTN_DV) {
-          if (!mbar_wait_warp(&b2full[s], (pc / S2) & 1)) { ok = false; break; }
-          clear(xb, t.len - t.at(n));
-        }
-        tc_fence_after();
-        if (lane == 0) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_bf16_ta(tmem + C::kColX, pa + k * 8, smem_desc_sw128(xb + k * 2048u, 8192u, 1024u), idx,
-                         (n == 0 && k == 0) ? 0u : 1u);
-          umma_commit(MODE == WATTN_DV ? &b2empty[s] : &b1empty[s]);
-          if (n + 1 == t.count) umma_commit(xfull);
+            umma_bf16(d, desc_at(a, kb * 16384 + k * 32), desc_at(yk, s * 16384 + k * 32), ids, (kb | k) ? 1u : 0u);
+          umma_commit(&yempty[s]);
         }
-        __syncwarp();
+        return true;
+      };
+      int ia = 0, g = 0, items = 0;                   // items begun, tiles, items with an accumulator
+      bool ok = true;
+      for (int item = blockIdx.x; ok && item < p.nitems; item += gridDim.x) {
+        const BwdItem<MODE> t(p, item);
+        if (t.count == 0) continue;
+        if (!mbar_wait(afull, ia & 1)) break;
+        ++ia;
+        for (int n = 0; ok && n < t.count; ++n, ++g) {
+          const int s = g % RX;
+          const bool last = n + 1 == t.count;
+          if constexpr (DV) {
+            // S(n + 1) goes over P(n - 1), behind the product that read it
+            for (int m = n ? n + 1 : 0; ok && m <= n + 1 && m < t.count; ++m) {
+              const int h = g - n + m;
+              if (!with_y(tmem + C::kColS + (h & 1) * 128, a1)) { ok = false; break; }
+              umma_commit(&sfull[h & 1]);
+              if (m + 1 == t.count) umma_commit(aempty);
+            }
+            if (!ok) break;
+          } else {
+            // dP(0): no tile before it; its buffer was read in the last item
+            if (n == 0) {
+              if (g > 0 && !mbar_wait(dread, (g - 1) & 1)) { ok = false; break; }
+              if (!with_y(tmem + C::kColD, a2)) { ok = false; break; }
+              umma_commit(dfull);
+            }
+            if (!mbar_wait(&xfull[s], (g / RX) & 1)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_bf16(tmem + C::kColS, desc_at(a1, kb * 16384 + k * 32),
+                          desc_at(xk, s * C::kTile + kb * 16384 + k * 32), ids, (kb | k) ? 1u : 0u);
+            umma_commit(sfull);
+            if (!last) {
+              if (!mbar_wait(dread, g & 1) || !with_y(tmem + C::kColD, a2)) { ok = false; break; }
+              umma_commit(dfull);
+            } else {
+              umma_commit(aempty);
+            }
+          }
+          if (n == 0 && items > 0 && !mbar_wait(gempty, (items - 1) & 1)) { ok = false; break; }
+          if (DV && !mbar_wait(&xfull[s], (g / RX) & 1)) { ok = false; break; }
+          if (!mbar_wait(DV ? &pfull[g & 1] : pfull, DV ? (g >> 1) & 1 : g & 1)) { ok = false; break; }
+          const uint32_t pa = tmem + C::kColS + (DV ? (g & 1) * 128 : 0);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_ta(tmem + C::kColX, pa + (k >> 2) * 64 + (k & 3) * 8, desc_at(xm, s * C::kTile + k * 2048), idx,
+                         (n == 0 && k == 0) ? 0u : 1u);
+          umma_commit(&xempty[s]);
+          if (last) umma_commit(gfull);
+        }
+        ++items;
       }
-      ++icx;
     }
   } else {
     // ---------------------------------------------------------- elementwise
-    const int group = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int half = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t ts = tq + C::kColS + group * 128;
+    const uint32_t td = tq + C::kColD + half * 64;
     const float c2 = p.a.scale * 1.4426950408889634f;
     const int window = p.a.window, sinks = p.a.sinks;
-    float* cols = reinterpret_cast<float*>(smem + C::kOffCol) + group * 128;   // lse (log2), delta
-    const uint32_t col_s = smem_u32(cols);
-    int sc = 0, ic = 0;
+    // lse (log2) [128] and delta [128] of a tile's columns; dV: lse of two tiles
+    float* cols = reinterpret_cast<float*>(smem + C::kOffCol);
+    const int mycol = threadIdx.x - 64;                          // 0..255
+    int g = 0, ic = 0;
     bool ok = true;
     for (int item = blockIdx.x; ok && item < p.nitems; item += gridDim.x) {
       const BwdItem<MODE> t(p, item);
@@ -311,26 +303,50 @@ __global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ Wa
         rl = p.a.lse[at] * 1.4426950408889634f;
         rd = p.a.delta[at];
       }
-      for (int n = 0; n < t.count; ++n, ++sc) {
-        if ((sc & 1) != group) continue;
-        const int b0 = t.at(n);                       // position of the tile's first column
+      for (int n = 0; n < t.count; ++n, ++g) {
+        const int t0 = t.at(n), b0 = t0 + half * 64;  // positions of the tile's and of this half's first column
+        const uint32_t ts = tq + C::kColS + (DV ? (g & 1) * 128 : 0) + half * 64;
+        const uint32_t col_s = smem_u32(cols) + (DV ? (g & 1) * 512 : 0) + half * 256;
         float x = 0.f;
         if (MODE != WATTN_DQ) {
           // the columns' statistics: one value per thread
-          const int i = b0 + (r & 63);
-          if (i < t.hi) {
+          const int i = t0 + (mycol & 127);
+          if (i < t.hi && (MODE == WATTN_DK || mycol < 128)) {
             const int64_t at = (static_cast<int64_t>(t.b) * p.a.H + t.head(n)) * p.a.Tq + i - off;
-            x = r < 64 ? p.a.lse[at] * 1.4426950408889634f : (MODE == WATTN_DK ? p.a.delta[at] : 0.f);
+            x = mycol < 128 ? p.a.lse[at] * 1.4426950408889634f : p.a.delta[at];
           }
         }
-        if (!mbar_wait_warp(&sfull[group], (sc >> 1) & 1)) { ok = false; break; }
-        if (MODE != WATTN_DQ) {
-          // S came after the group's last dS, so the last tile's statistics have been read
-          cols[r] = x;
+        float dp[64];
+        if (!DV) {
+          // dP first, so that its buffer is free while dS is computed
+          if (!mbar_wait_warp(dfull, g & 1)) { ok = false; break; }
+          tc_fence_after();
+          tmem_ld32(td, dp);
+          tmem_ld32(td + 32, dp + 32);
+          tmem_ld_wait();
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&cfull[group]);
-          if (!mbar_wait_warp(&cfull[group], (sc >> 1) & 1)) { ok = false; break; }
+          if (lane == 0) mbar_arrive(dread);
         }
+        if (!mbar_wait_warp(DV ? &sfull[g & 1] : sfull, DV ? (g >> 1) & 1 : g & 1)) { ok = false; break; }
+        if (MODE != WATTN_DQ) {
+          // dK: S came after the last dS, so the last tile's statistics have been
+          // read; dV: after the P before that, so this buffer's have
+          if (!DV) cols[mycol] = x;
+          else if (mycol < 128) cols[(g & 1) * 128 + mycol] = x;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(cfull);
+        }
+        // the last product's rows behind the sequence: a dS of 0 times whatever is there must stay 0
+        if (t.len < t0 + 128) {
+          const int s = g % RX, keep = max(t.len - t0, 0);
+          if (!mbar_wait_warp(&xfull[s], (g / RX) & 1)) { ok = false; break; }
+          const uint32_t xb = smem_u32(smem) + C::kOffX + s * C::kTile;
+          for (int e = keep * 8 + mycol; e < 1024; e += 256)
+            for (int kb = 0; kb < KB; ++kb) st_shared_v4(xb + kb * 16384 + e * 16, 0, 0, 0, 0);
+          fence_async_smem();
+        }
+        if (MODE != WATTN_DQ && !mbar_wait_warp(cfull, g & 1)) { ok = false; break; }
         tc_fence_after();
         bool whole;
         int clo, chi, csk;                            // columns c with clo < c <= chi, or csk's side
@@ -350,28 +366,22 @@ __global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ Wa
         uint32_t hw[32];
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 32) {
-          float s[32], dp[32];
-          tmem_ld16(ts + c0, s);
-          tmem_ld16(ts + c0 + 16, s + 16);
-          if (MODE != WATTN_DV) {
-            tmem_ld16(ts + 64 + c0, dp);
-            tmem_ld16(ts + 64 + c0 + 16, dp + 16);
-          }
+          float s[32];
+          tmem_ld32(ts + c0, s);
           tmem_ld_wait();
 #pragma unroll
-          for (int c4 = 0; c4 < 32; c4 += 4) {
-            float4 l4, d4;
+          for (int c = 0; c < 32; c += 4) {
+            float4 l4 = make_float4(rl, rl, rl, rl), d4 = make_float4(rd, rd, rd, rd);
             if (MODE != WATTN_DQ) {
-              asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(l4.x), "=f"(l4.y), "=f"(l4.z), "=f"(l4.w) : "r"(col_s + (c0 + c4) * 4));
+              asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(l4.x), "=f"(l4.y), "=f"(l4.z), "=f"(l4.w) : "r"(col_s + (c0 + c) * 4));
               if (MODE == WATTN_DK)
-                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(d4.x), "=f"(d4.y), "=f"(d4.z), "=f"(d4.w) : "r"(col_s + 256 + (c0 + c4) * 4));
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(d4.x), "=f"(d4.y), "=f"(d4.z), "=f"(d4.w) : "r"(col_s + 512 + (c0 + c) * 4));
             }
             const float ll[4] = {l4.x, l4.y, l4.z, l4.w}, dd[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int c = c4 + k;
-              const float pr = ex2_approx(fmaf(s[c], c2, -(MODE == WATTN_DQ ? rl : ll[k])));
-              s[c] = MODE == WATTN_DV ? pr : pr * (dp[c] - (MODE == WATTN_DQ ? rd : dd[k]));
+              const float pr = ex2_approx(fmaf(s[c + k], c2, -ll[k]));
+              s[c + k] = DV ? pr : pr * (dp[c0 + c + k] - dd[k]);
             }
           }
           if (!whole) {
@@ -383,21 +393,22 @@ __global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ Wa
 #pragma unroll
           for (int c = 0; c < 16; ++c) hw[c0 / 2 + c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
         }
+        // over the first half of the 64 columns that this thread has read
         tmem_st16u(ts, hw);
         tmem_st16u(ts + 16, hw + 16);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[group]);
+        if (lane == 0) mbar_arrive(DV ? &pfull[g & 1] : pfull);
       }
       if (!ok) break;
-      // the gradient's rows: this group's half of the channels
+      // the gradient's rows: this half of the channels
       if (t.count > 0) {
-        if (!mbar_wait_warp(xfull, ic & 1)) break;
+        if (!mbar_wait_warp(gfull, ic & 1)) break;
         ++ic;
         tc_fence_after();
       }
-      const float mul = MODE == WATTN_DV ? 1.0f : p.a.scale;
+      const float mul = DV ? 1.0f : p.a.scale;
       const int row = t.a0 + r;
       const bool in = row < (MODE == WATTN_DQ ? p.a.Tq : p.a.T);
       const bool zero = t.count == 0 || (MODE == WATTN_DQ && mine >= t.len);
@@ -407,23 +418,23 @@ __global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ Wa
       float* pd = nullptr;
       if (partial)
         pd = p.a.part + ((((static_cast<int64_t>(t.b) * p.a.Hkv + t.ha) * p.sink_tiles + t.kt) * p.parts + t.part) * 2 +
-                         (MODE == WATTN_DV ? 1 : 0)) * (128 * D) + r * D;
+                         (DV ? 1 : 0)) * (128 * D) + r * D;
 #pragma unroll 1
-      for (int c0 = group * (D / 2); c0 < (group + 1) * (D / 2); c0 += 16) {
-        float x[16];
+      for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+        float x[32];
         if (t.count > 0) {
           __syncwarp();
-          tmem_ld16(tq + C::kColX + c0, x);
+          tmem_ld32(tq + C::kColX + c0, x);
           tmem_ld_wait();
         }
 #pragma unroll
-        for (int c = 0; c < 16; ++c) x[c] = zero ? 0.f : x[c] * mul;
+        for (int c = 0; c < 32; ++c) x[c] = zero ? 0.f : x[c] * mul;
         if (partial) {
 #pragma unroll
-          for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(pd + c0 + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+          for (int c = 0; c < 32; c += 4) *reinterpret_cast<float4*>(pd + c0 + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
         } else if (in) {
 #pragma unroll
-          for (int c = 0; c < 16; c += 8)
+          for (int c = 0; c < 32; c += 8)
             if (c0 + c < p.a.d)
               st_global_v4(dst + c0 + c, pack_bf16x2(x[c], x[c + 1]), pack_bf16x2(x[c + 2], x[c + 3]),
                            pack_bf16x2(x[c + 4], x[c + 5]), pack_bf16x2(x[c + 6], x[c + 7]));
@@ -432,7 +443,7 @@ __global__ void __launch_bounds__(320, 1) k_wattn_bwd(const __grid_constant__ Wa
       if (t.count > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(xempty);
+        if (lane == 0) mbar_arrive(gempty);
       }
     }
   }

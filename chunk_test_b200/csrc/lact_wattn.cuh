@@ -310,10 +310,16 @@ static cudaError_t wattn_bwd_bf16(const WattnDims& D, const WattnParams& a, cuda
     default: { constexpr int DP = 256; return __VA_ARGS__; }  \
   }
 
+template <typename T, int LANES>
+static cudaError_t launch_wattn_delta_as(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(cdiv(D.B * D.H * D.Tq, 256 / LANES), kPlanSMs * 32)));
+  return launch_pdl(k_wattn_delta<T, LANES>, grid, dim3(256), 0, st, a);
+}
 static cudaError_t launch_wattn_delta(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(cdiv(D.B * D.H * D.Tq, 8), kPlanSMs * 16)));
-  return D.dtype == LACT_F32 ? launch_pdl(k_wattn_delta<float>, grid, dim3(256), 0, st, a)
-                             : launch_pdl(k_wattn_delta<__nv_bfloat16>, grid, dim3(256), 0, st, a);
+  using B16 = __nv_bfloat16;
+  if (D.dtype == LACT_F32) return launch_wattn_delta_as<float, 32>(D, a, st);
+  if (D.d <= 64) return launch_wattn_delta_as<B16, 8>(D, a, st);
+  return D.d <= 128 ? launch_wattn_delta_as<B16, 16>(D, a, st) : launch_wattn_delta_as<B16, 32>(D, a, st);
 }
 static cudaError_t launch_wattn_sums(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
   const int64_t n = D.B * D.Hkv * D.sink_tiles * 2 * D.bn * (D.DP / 4);
@@ -359,17 +365,19 @@ static int decode_validate(const lact_swa_sink_problem* p) {
 }
 
 // CTAs of one (sequence, key head): doubled while the whole grid would leave
-// SMs idle and each CTA keeps a block of 16 slots for each of its warps.
+// SMs idle and each CTA keeps 16 slots for each of its warps.  More CTAs than
+// that cost more in joining than they balance (64 sequences, 4 key heads, d 128,
+// windows of 8192: 189 us with one, 257 us with four).  16 is the largest cluster.
 static int decode_ranks(int64_t items, int64_t slots) {
   int r = 1;
-  while (r < 8 && items * r < kPlanSMs && slots > static_cast<int64_t>(r) * kDecWarps * 16) r *= 2;
+  while (r < 16 && items * r < kPlanSMs && slots >= static_cast<int64_t>(r) * 2 * kDecWarps * 16) r *= 2;
   return r;
 }
 
 template <class F>
 static cudaError_t launch_decode_as(F* kernel, int smem, bool (&done)[64], const DecodeParams& a, int64_t items,
                                     cudaStream_t st) {
-  cudaError_t e = set_smem(kernel, smem, done);
+  cudaError_t e = set_smem(kernel, smem, done, true);
   if (e != cudaSuccess) return e;
   const int ranks = decode_ranks(items, static_cast<int64_t>(a.sinks) + a.window);
   cudaLaunchConfig_t cfg = {};

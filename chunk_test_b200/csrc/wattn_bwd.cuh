@@ -18,12 +18,13 @@
 //   warp 0      TMA producer of A and B1.
 //   warp 10     TMA producer of B2.
 //   warp 1      issues S = A1 B1^T, dP = A2 B2^T and dX += dS B1 (dV: P B2),
-//               dS in TMEM in bf16 over S.  One thread, in the order
-//               S(n), dP(n+1) once dP(n) has been read, dX(n): the tensor pipe
-//               forms dP(n+1) while dS(n) is computed.
+//               dS in TMEM in bf16 over S.  One thread; the tensor pipe forms
+//               dP(n+1), and S(n+1) where TMEM holds two (d <= 128, dV), while
+//               dS(n) is computed.
 //   warps 2-9   dS (dV: P): two threads per row, 64 columns each.
-// Bound by the tensor pipe; at d = 256 shared memory holds one B1 tile, so its
-// load is exposed in part.
+// Bound by the elementwise work up to d = 128 (a tile has 16384 exponentials, 1024
+// clocks, and as many differences and products); at d = 256 by the chain S, dS, dX of
+// one tile, for TMEM holds one S beside 256 columns of dX, and shared memory one B1.
 #pragma once
 
 #include "wattn_fwd.cuh"
@@ -91,6 +92,7 @@ template <int D, int MODE>
 struct BwdCfg {
   static constexpr int kKb = D / 64;
   static constexpr bool kDv = MODE == WATTN_DV;
+  static constexpr int kSB = kDv || D <= 128 ? 2 : 1;      // buffers of S (and of dS or P, which go over it)
   static constexpr int kABytes = kKb * 16384;
   static constexpr int kAll = kDv ? kABytes : 2 * kABytes;
   static constexpr int kTile = kKb * 16384;                // a B tile of 128 rows
@@ -102,26 +104,27 @@ struct BwdCfg {
   static constexpr int kRy0 = kBlocks - kRx * kKb, kRy = kRy0 > 2 * kKb ? 2 * kKb : kRy0;
   static_assert(kRy >= 2, "room for two blocks");
   static constexpr int kOffX = kAll, kOffY = kOffX + kRx * kTile, kOffCol = kOffY + kRy * 16384;
-  static constexpr int kOffBar = kOffCol + 2 * 128 * 4;    // lse and delta of a tile's columns
-  // afull aempty | xfull[] xempty[] | yfull[] yempty[] | sfull dfull pfull dread cfull | gfull gempty
-  // (dV: S and P have two buffers, sfull[2] and pfull[2])
-  static constexpr int kBars = 2 + 2 * kRx + 2 * kRy + 5 + 2;
+  static constexpr int kCol = kDv ? 128 : 256,   // lse and delta of a tile's columns
+      kOffBar = kOffCol + kSB * kCol * 4;
+  // afull aempty | xfull[] xempty[] | yfull[] yempty[] | sfull[SB] pfull[SB] dfull dread cfull | gfull gempty
+  static constexpr int kBars = 2 + 2 * kRx + 2 * kRy + 2 * kSB + 3 + 2;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
   static constexpr int kThreads = 352;
-  static constexpr uint32_t kColX = 0, kColS = 256, kColD = 384;
+  // columns: the accumulator, S, dP (dV has none)
+  static constexpr uint32_t kColX = 0, kColS = 256, kColD = kSB == 2 ? 128 : 384;
 };
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ WattnBwdParams p) {
   using C = BwdCfg<D, MODE>;
-  constexpr int RX = C::kRx, RY = C::kRy, KB = C::kKb;
+  constexpr int RX = C::kRx, RY = C::kRy, KB = C::kKb, SB = C::kSB;
   constexpr bool DV = C::kDv;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *afull = bar, *aempty = bar + 1, *xfull = bar + 2, *xempty = xfull + RX, *yfull = xempty + RX,
-           *yempty = yfull + RY, *sfull = yempty + RY, *dfull = sfull + 1, *pfull = dfull + 1, *dread = pfull + 1,
-           *cfull = dread + 1, *gfull = cfull + 1, *gempty = gfull + 1;
+           *yempty = yfull + RY, *sfull = yempty + RY, *pfull = sfull + SB, *dfull = pfull + SB,
+           *dread = dfull + 1, *cfull = dread + 1, *gfull = cfull + 1, *gempty = gfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + C::kBars);
 
   griddep_launch();
@@ -138,10 +141,12 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
       mbar_init(&yfull[i], 1);
       mbar_init(&yempty[i], 1);
     }
-    mbar_init(sfull, 1);
+    for (int i = 0; i < SB; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 8);
+    }
     mbar_init(dfull, 1);
     mbar_init(dread, 8);
-    mbar_init(pfull, 8);
     mbar_init(cfull, 8);
     mbar_init(gfull, 1);
     mbar_init(gempty, 8);
@@ -245,32 +250,40 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
             }
             if (!ok) break;
           } else {
-            // dP(0): no tile before it; its buffer was read in the last item
+            // S(h) goes over dS(h - SB), behind the product that read it
+            auto with_x = [&](int h) -> bool {
+              const int x = h % RX;
+              if (!mbar_wait(&xfull[x], (h / RX) & 1)) return false;
+              tc_fence_after();
+#pragma unroll
+              for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  umma_bf16(tmem + C::kColS + (h % SB) * 128, desc_at(a1, kb * 16384 + k * 32),
+                            desc_at(xk, x * C::kTile + kb * 16384 + k * 32), ids, (kb | k) ? 1u : 0u);
+              umma_commit(&sfull[h % SB]);
+              return true;
+            };
             if (n == 0) {
               if (g > 0 && !mbar_wait(dread, (g - 1) & 1)) { ok = false; break; }
               if (!with_y(tmem + C::kColD, a2)) { ok = false; break; }
               umma_commit(dfull);
             }
-            if (!mbar_wait(&xfull[s], (g / RX) & 1)) { ok = false; break; }
-            tc_fence_after();
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_bf16(tmem + C::kColS, desc_at(a1, kb * 16384 + k * 32),
-                          desc_at(xk, s * C::kTile + kb * 16384 + k * 32), ids, (kb | k) ? 1u : 0u);
-            umma_commit(sfull);
+            if (n == 0 || SB == 1) {
+              if (!with_x(g)) { ok = false; break; }
+              if (last) umma_commit(aempty);
+            }
             if (!last) {
+              if (SB == 2 && !with_x(g + 1)) { ok = false; break; }
               if (!mbar_wait(dread, g & 1) || !with_y(tmem + C::kColD, a2)) { ok = false; break; }
               umma_commit(dfull);
-            } else {
-              umma_commit(aempty);
+              if (SB == 2 && n + 2 == t.count) umma_commit(aempty);
             }
           }
           if (n == 0 && items > 0 && !mbar_wait(gempty, (items - 1) & 1)) { ok = false; break; }
           if (DV && !mbar_wait(&xfull[s], (g / RX) & 1)) { ok = false; break; }
-          if (!mbar_wait(DV ? &pfull[g & 1] : pfull, DV ? (g >> 1) & 1 : g & 1)) { ok = false; break; }
-          const uint32_t pa = tmem + C::kColS + (DV ? (g & 1) * 128 : 0);
+          if (!mbar_wait(&pfull[g % SB], (g / SB) & 1)) { ok = false; break; }
+          const uint32_t pa = tmem + C::kColS + (g % SB) * 128;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -289,7 +302,7 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
     const uint32_t td = tq + C::kColD + half * 64;
     const float c2 = p.a.scale * 1.4426950408889634f;
     const int window = p.a.window, sinks = p.a.sinks;
-    // lse (log2) [128] and delta [128] of a tile's columns; dV: lse of two tiles
+    // lse (log2) [128] and delta [128] of a tile's columns, as many as there are S buffers
     float* cols = reinterpret_cast<float*>(smem + C::kOffCol);
     const int mycol = threadIdx.x - 64;                          // 0..255
     int g = 0, ic = 0;
@@ -305,8 +318,8 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
       }
       for (int n = 0; n < t.count; ++n, ++g) {
         const int t0 = t.at(n), b0 = t0 + half * 64;  // positions of the tile's and of this half's first column
-        const uint32_t ts = tq + C::kColS + (DV ? (g & 1) * 128 : 0) + half * 64;
-        const uint32_t col_s = smem_u32(cols) + (DV ? (g & 1) * 512 : 0) + half * 256;
+        const uint32_t ts = tq + C::kColS + (g % SB) * 128 + half * 64;
+        const uint32_t col_s = smem_u32(cols) + (g % SB) * C::kCol * 4 + half * 256;
         float x = 0.f;
         if (MODE != WATTN_DQ) {
           // the columns' statistics: one value per thread
@@ -328,12 +341,10 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
           __syncwarp();
           if (lane == 0) mbar_arrive(dread);
         }
-        if (!mbar_wait_warp(DV ? &sfull[g & 1] : sfull, DV ? (g >> 1) & 1 : g & 1)) { ok = false; break; }
+        if (!mbar_wait_warp(&sfull[g % SB], (g / SB) & 1)) { ok = false; break; }
         if (MODE != WATTN_DQ) {
-          // dK: S came after the last dS, so the last tile's statistics have been
-          // read; dV: after the P before that, so this buffer's have
-          if (!DV) cols[mycol] = x;
-          else if (mycol < 128) cols[(g & 1) * 128 + mycol] = x;
+          // S came after the last dS from this buffer, so its statistics have been read
+          if (mycol < C::kCol) cols[(g % SB) * C::kCol + mycol] = x;
           __syncwarp();
           if (lane == 0) mbar_arrive(cfull);
         }
@@ -399,7 +410,7 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(DV ? &pfull[g & 1] : pfull);
+        if (lane == 0) mbar_arrive(&pfull[g % SB]);
       }
       if (!ok) break;
       // the gradient's rows: this half of the channels

@@ -155,7 +155,7 @@ __device__ __forceinline__ void decode_write(const DecodeParams& p, const Decode
 // from the cache: nothing is staged.  Tensor throughput is no limit here; the
 // instruction is used because 8 heads on the CUDA cores would be.
 template <int DP>
-__global__ void __launch_bounds__(kDecThreads, 1) k_wattn_decode_bf16(const DecodeParams p) {
+__global__ void __launch_bounds__(kDecThreads, DP <= 128 ? 2 : 1) k_wattn_decode_bf16(const DecodeParams p) {
   using B16 = __nv_bfloat16;
   extern __shared__ float dec_smem[];
   float *wm = dec_smem, *wl = wm + kDecWarps * kDecHeads, *wacc = wl + kDecWarps * kDecHeads;

@@ -176,31 +176,35 @@ __global__ void __launch_bounds__(kSimtThreads) k_wattn_fwd_f32(const WattnParam
   }
 }
 
-// delta[b, h, t] = sum_c dout out, one warp per row, in 32 bits; 0 past the length
-template <typename T>
+// delta[b, h, t] = sum_c dout out in 32 bits; 0 past the length.  LANES lanes of
+// a warp per row, 16 bytes each at a time.
+template <typename T, int LANES>
 __global__ void __launch_bounds__(256) k_wattn_delta(const WattnParams p) {
   griddep_launch();
   griddep_wait();
   const int64_t rows = static_cast<int64_t>(p.B) * p.H * p.Tq;
-  const int lane = threadIdx.x & 31;
-  constexpr int kV = 16 / sizeof(T);
-  for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8) {
-    const int t = static_cast<int>(row % p.Tq), bh = static_cast<int>(row / p.Tq), b = bh / p.H, h = bh % p.H;
+  constexpr int kV = 16 / sizeof(T), kRows = 256 / LANES;
+  const int lane = threadIdx.x % LANES;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t row = r0 + threadIdx.x / LANES;
     float s = 0.f;
-    if (t + p.T - p.Tq < seq_len(p, b)) {
-      const T* o = static_cast<const T*>(p.out.p) + b * p.out.sb + h * p.out.sh + t * p.out.st;
-      const T* g = static_cast<const T*>(p.dout.p) + b * p.dout.sb + h * p.dout.sh + t * p.dout.st;
-      for (int c = lane * kV; c < p.d; c += 32 * kV) {
-        float x[kV], y[kV];
-        load_vec<kV>(o + c, x);
-        load_vec<kV>(g + c, y);
+    if (row < rows) {
+      const int t = static_cast<int>(row % p.Tq), bh = static_cast<int>(row / p.Tq), b = bh / p.H, h = bh % p.H;
+      if (t + p.T - p.Tq < seq_len(p, b)) {
+        const T* o = static_cast<const T*>(p.out.p) + b * p.out.sb + h * p.out.sh + t * p.out.st;
+        const T* g = static_cast<const T*>(p.dout.p) + b * p.dout.sb + h * p.dout.sh + t * p.dout.st;
+        for (int c = lane * kV; c < p.d; c += LANES * kV) {
+          float x[kV], y[kV];
+          load_vec<kV>(o + c, x);
+          load_vec<kV>(g + c, y);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) s = fmaf(x[i], y[i], s);
+          for (int i = 0; i < kV; ++i) s = fmaf(x[i], y[i], s);
+        }
       }
     }
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    if (lane == 0) p.delta[row] = s;
+    for (int x = LANES / 2; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (row < rows && lane == 0) p.delta[row] = s;
   }
 }
 

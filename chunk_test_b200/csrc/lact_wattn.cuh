@@ -289,7 +289,8 @@ static cudaError_t wattn_bwd_bf16(const WattnDims& D, const WattnParams& a, cuda
   CUtensorMap *q = MODE == WATTN_DQ ? &f.tmA1 : &f.tmB1, *g = MODE == WATTN_DQ ? &f.tmA2 : &f.tmB2;
   CUtensorMap *k = MODE == WATTN_DQ ? &f.tmB1 : &f.tmA1, *v = MODE == WATTN_DQ ? &f.tmB2 : &f.tmA2;
   if (!map_view(q, a.q, eq, 128) || !map_view(g, a.dout, eq, 128) || !map_view(k, a.k, ek, 128) ||
-      !map_view(v, a.v, ek, 128))
+      !map_view(v, a.v, ek, 128) ||
+      !(MODE == WATTN_DQ ? map_view(&f.tmX64, a.k, ek, 64) : map_view(&f.tmX64, MODE == WATTN_DK ? a.q : a.dout, eq, 64)))
     return cudaErrorInvalidValue;
   f.a = a;
   f.sink_tiles = D.sink_tiles;

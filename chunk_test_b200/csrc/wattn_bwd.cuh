@@ -36,6 +36,7 @@ enum WattnMode { WATTN_DQ, WATTN_DK, WATTN_DV };
 struct WattnBwdParams {
   CUtensorMap tmA1, tmA2;   // q, dout (dQ) or k, v (dK, dV), box {64, 128}
   CUtensorMap tmB1, tmB2;   // k, v (dQ) or q, dout (dK, dV), box {64, 128}
+  CUtensorMap tmX64;        // B1 (dV: B2), box {64, 64}
   WattnParams a;
   int nitems, per_head;     // items in all, and per (batch, head of A)
   int sink_tiles, parts;    // dK, dV: the split of the sink tiles (KeyPart)
@@ -93,21 +94,27 @@ struct BwdCfg {
   static constexpr int kKb = D / 64;
   static constexpr bool kDv = MODE == WATTN_DV;
   static constexpr int kSB = kDv || D <= 128 ? 2 : 1;      // buffers of S (and of dS or P, which go over it)
+  static constexpr int kCol = kDv ? 128 : MODE == WATTN_DK ? 256 : 0;   // lse and delta of a tile's columns
   static constexpr int kABytes = kKb * 16384;
   static constexpr int kAll = kDv ? kABytes : 2 * kABytes;
+  // two sets of resident operands where they fit: the next item's first tile is
+  // begun under this item's last
+  static constexpr int kRA = D == 64 ? 2 : 1;
   static constexpr int kTile = kKb * 16384;                // a B tile of 128 rows
   // The operand of the last product (B1; dV: B2) stays until that product is
   // done: whole tiles.  The other one is K-major only and goes by blocks of 64
   // channels.
-  static constexpr int kBlocks = (229376 - kAll) / 16384;  // 16 KB blocks there is room for
-  static constexpr int kRx = kBlocks >= 2 * kKb + 2 ? 2 : 1;
+  static constexpr int kBlocks = (230400 - kSB * kCol * 4 - kRA * kAll) / 16384;  // 16 KB blocks there is room for
+  static constexpr int kRx = kBlocks >= 3 * kKb + 2 ? 3 : kBlocks >= 2 * kKb + 2 ? 2 : 1;
+  // a single X slot is refilled by halves of 64 rows: the product that reads it
+  // is done with the first half before the second
+  static constexpr int kHx = kRx == 1 ? 2 : 1;
   static constexpr int kRy0 = kBlocks - kRx * kKb, kRy = kRy0 > 2 * kKb ? 2 * kKb : kRy0;
   static_assert(kRy >= 2, "room for two blocks");
-  static constexpr int kOffX = kAll, kOffY = kOffX + kRx * kTile, kOffCol = kOffY + kRy * 16384;
-  static constexpr int kCol = kDv ? 128 : 256,   // lse and delta of a tile's columns
-      kOffBar = kOffCol + kSB * kCol * 4;
-  // afull aempty | xfull[] xempty[] | yfull[] yempty[] | sfull[SB] pfull[SB] dfull dread cfull | gfull gempty
-  static constexpr int kBars = 2 + 2 * kRx + 2 * kRy + 2 * kSB + 3 + 2;
+  static constexpr int kOffX = kRA * kAll, kOffY = kOffX + kRx * kTile, kOffCol = kOffY + kRy * 16384;
+  static constexpr int kOffBar = kOffCol + kSB * kCol * 4;
+  // afull[RA] aempty[RA] | xfull[] xempty[] | yfull[] yempty[] | sfull[SB] pfull[SB] dfull dread cfull | gfull gempty
+  static constexpr int kBars = 2 * kRA + kRx + kRx * kHx + 2 * kRy + 2 * kSB + 3 + 2;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
   static constexpr int kThreads = 352;
   // columns: the accumulator, S, dP (dV has none)
@@ -117,12 +124,12 @@ struct BwdCfg {
 template <int D, int MODE>
 __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ WattnBwdParams p) {
   using C = BwdCfg<D, MODE>;
-  constexpr int RX = C::kRx, RY = C::kRy, KB = C::kKb, SB = C::kSB;
+  constexpr int RX = C::kRx, RY = C::kRy, KB = C::kKb, SB = C::kSB, RA = C::kRA, HX = C::kHx;
   constexpr bool DV = C::kDv;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t *afull = bar, *aempty = bar + 1, *xfull = bar + 2, *xempty = xfull + RX, *yfull = xempty + RX,
+  uint64_t *afull = bar, *aempty = afull + RA, *xfull = aempty + RA, *xempty = xfull + RX, *yfull = xempty + RX * HX,
            *yempty = yfull + RY, *sfull = yempty + RY, *pfull = sfull + SB, *dfull = pfull + SB,
            *dread = dfull + 1, *cfull = dread + 1, *gfull = cfull + 1, *gempty = gfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + C::kBars);
@@ -131,11 +138,13 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (__syncthreads_or(*reinterpret_cast<volatile int*>(&g_status))) return;   // an earlier wait gave up
   if (threadIdx.x == 0) {
-    mbar_init(afull, 1);
-    mbar_init(aempty, 1);
+    for (int i = 0; i < RA; ++i) {
+      mbar_init(&afull[i], 1);
+      mbar_init(&aempty[i], 1);
+    }
     for (int i = 0; i < RX; ++i) {
       mbar_init(&xfull[i], 1);
-      mbar_init(&xempty[i], 1);
+      for (int k = 0; k < HX; ++k) mbar_init(&xempty[i * HX + k], 1);
     }
     for (int i = 0; i < RY; ++i) {
       mbar_init(&yfull[i], 1);
@@ -172,29 +181,35 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
     // X: the operand of the last product, whole tiles; Y: the other one, by blocks
     if (lane == 0) {
       const bool x = warp == 0;
-      const CUtensorMap* map = (x != DV) ? &p.tmB1 : &p.tmB2;
+      // X by boxes of 128 / HX rows, Y of 128
+      const CUtensorMap* map = x ? (HX == 2 ? &p.tmX64 : DV ? &p.tmB2 : &p.tmB1) : DV ? &p.tmB1 : &p.tmB2;
       int ib = 0, ic = 0;
       bool ok = true;
       for (int item = blockIdx.x; ok && item < p.nitems; item += gridDim.x) {
         const BwdItem<MODE> t(p, item);
         if (t.count == 0) continue;
         if (x) {
-          if (ic > 0 && !mbar_wait(aempty, (ic - 1) & 1)) break;
+          const int s = ic % RA;
+          if (ic >= RA && !mbar_wait(&aempty[s], ((ic / RA) - 1) & 1)) break;
           ++ic;
-          mbar_arrive_expect_tx(afull, C::kAll);
+          mbar_arrive_expect_tx(&afull[s], C::kAll);
           for (int kb = 0; kb < KB; ++kb) {
-            tma_load_4d(smem + kb * 16384, &p.tmA1, afull, kb * 64, t.a0, t.ha, t.b);
-            if (!DV) tma_load_4d(smem + C::kABytes + kb * 16384, &p.tmA2, afull, kb * 64, t.a0, t.ha, t.b);
+            uint8_t* dst = smem + s * C::kAll + kb * 16384;
+            tma_load_4d(dst, &p.tmA1, &afull[s], kb * 64, t.a0, t.ha, t.b);
+            if (!DV) tma_load_4d(dst + C::kABytes, &p.tmA2, &afull[s], kb * 64, t.a0, t.ha, t.b);
           }
         }
         for (int n = 0; ok && n < t.count; ++n) {
           const int row = t.at(n) - (MODE == WATTN_DQ ? 0 : off), hb = t.head(n);
           if (x) {
             const int s = ib % RX;
-            if (ib >= RX && !mbar_wait(&xempty[s], ((ib / RX) - 1) & 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(&xfull[s], C::kTile);
-            for (int kb = 0; kb < KB; ++kb)
-              tma_load_4d(smem + C::kOffX + s * C::kTile + kb * 16384, map, &xfull[s], kb * 64, row, hb, t.b);
+            for (int k = 0; ok && k < HX; ++k) {
+              if (ib >= RX && !mbar_wait(&xempty[s * HX + k], ((ib / RX) - 1) & 1)) { ok = false; break; }
+              if (k == 0) mbar_arrive_expect_tx(&xfull[s], C::kTile);
+              for (int kb = 0; kb < KB; ++kb)
+                tma_load_4d(smem + C::kOffX + s * C::kTile + kb * 16384 + k * 8192, map, &xfull[s], kb * 64,
+                            row + k * 64, hb, t.b);
+            }
             ++ib;
           } else {
             for (int kb = 0; kb < KB; ++kb, ++ib) {
@@ -217,80 +232,96 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
                      xm = smem_desc_sw128(sbase + C::kOffX, 16384u, 1024u),
                      yk = smem_desc_sw128(sbase + C::kOffY, 16u, 1024u);
       int iy = 0;
-      // the product of a resident operand with the next tile of Y, by blocks
-      auto with_y = [&](uint32_t d, uint64_t a) -> bool {
+      // S of tile h in all, with the tile X(h) (dV: with Y)
+      auto with_x = [&](int h, int abuf) -> bool {
+        const int x = h % RX;
+        if (!mbar_wait(&xfull[x], (h / RX) & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tmem + C::kColS + (h % SB) * 128, desc_at(a1, abuf * C::kAll + kb * 16384 + k * 32),
+                      desc_at(xk, x * C::kTile + kb * 16384 + k * 32), ids, (kb | k) ? 1u : 0u);
+        umma_commit(&sfull[h % SB]);
+        return true;
+      };
+      // a resident operand with the next tile of Y, by blocks
+      auto with_y = [&](uint32_t d, uint64_t a, int abuf) -> bool {
         for (int kb = 0; kb < KB; ++kb, ++iy) {
           const int s = iy % RY;
           if (!mbar_wait(&yfull[s], (iy / RY) & 1)) return false;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_bf16(d, desc_at(a, kb * 16384 + k * 32), desc_at(yk, s * 16384 + k * 32), ids, (kb | k) ? 1u : 0u);
+            umma_bf16(d, desc_at(a, abuf * C::kAll + kb * 16384 + k * 32), desc_at(yk, s * 16384 + k * 32), ids,
+                      (kb | k) ? 1u : 0u);
           umma_commit(&yempty[s]);
         }
         return true;
       };
-      int ia = 0, g = 0, items = 0;                   // items begun, tiles, items with an accumulator
-      bool ok = true;
+      // The tile whose S (and dP) is next: `ahead` of the one whose dX is, by one
+      // tile, over the items' ends too where there are two sets of A.
+      int nt = blockIdx.x, nn = 0, ncount = 0, ia = 0, h = 0;
+      auto settle = [&]() {
+        while (nt < p.nitems && (ncount = BwdItem<MODE>(p, nt).count) == 0) nt += gridDim.x;
+      };
+      // dP (and S, where TMEM holds two) of the next tile; S alone
+      auto next_d = [&]() -> bool {
+        if (nn == 0 && !mbar_wait(&afull[ia % RA], (ia / RA) & 1)) return false;
+        if constexpr (DV) {
+          if (!with_y(tmem + C::kColS + (h % SB) * 128, a1, ia % RA)) return false;
+          umma_commit(&sfull[h % SB]);
+        } else {
+          if (SB == 2 && !with_x(h, ia % RA)) return false;
+          if (h > 0 && !mbar_wait(dread, (h - 1) & 1)) return false;   // the last dP has been read
+          if (!with_y(tmem + C::kColD, a2, ia % RA)) return false;
+          umma_commit(dfull);
+        }
+        return true;
+      };
+      auto next_done = [&]() {
+        if (nn + 1 == ncount) {
+          umma_commit(&aempty[ia % RA]);
+          ++ia;
+          nn = 0;
+          nt += gridDim.x;
+          settle();
+        } else {
+          ++nn;
+        }
+        ++h;
+      };
+      settle();
+      int g = 0, items = 0;                           // tiles, items with an accumulator
+      bool ok = true, begun = false;
       for (int item = blockIdx.x; ok && item < p.nitems; item += gridDim.x) {
         const BwdItem<MODE> t(p, item);
         if (t.count == 0) continue;
-        if (!mbar_wait(afull, ia & 1)) break;
-        ++ia;
         for (int n = 0; ok && n < t.count; ++n, ++g) {
-          const int s = g % RX;
-          const bool last = n + 1 == t.count;
-          if constexpr (DV) {
-            // S(n + 1) goes over P(n - 1), behind the product that read it
-            for (int m = n ? n + 1 : 0; ok && m <= n + 1 && m < t.count; ++m) {
-              const int h = g - n + m;
-              if (!with_y(tmem + C::kColS + (h & 1) * 128, a1)) { ok = false; break; }
-              umma_commit(&sfull[h & 1]);
-              if (m + 1 == t.count) umma_commit(aempty);
-            }
-            if (!ok) break;
-          } else {
-            // S(h) goes over dS(h - SB), behind the product that read it
-            auto with_x = [&](int h) -> bool {
-              const int x = h % RX;
-              if (!mbar_wait(&xfull[x], (h / RX) & 1)) return false;
-              tc_fence_after();
-#pragma unroll
-              for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_bf16(tmem + C::kColS + (h % SB) * 128, desc_at(a1, kb * 16384 + k * 32),
-                            desc_at(xk, x * C::kTile + kb * 16384 + k * 32), ids, (kb | k) ? 1u : 0u);
-              umma_commit(&sfull[h % SB]);
-              return true;
-            };
-            if (n == 0) {
-              if (g > 0 && !mbar_wait(dread, (g - 1) & 1)) { ok = false; break; }
-              if (!with_y(tmem + C::kColD, a2)) { ok = false; break; }
-              umma_commit(dfull);
-            }
-            if (n == 0 || SB == 1) {
-              if (!with_x(g)) { ok = false; break; }
-              if (last) umma_commit(aempty);
-            }
-            if (!last) {
-              if (SB == 2 && !with_x(g + 1)) { ok = false; break; }
-              if (!mbar_wait(dread, g & 1) || !with_y(tmem + C::kColD, a2)) { ok = false; break; }
-              umma_commit(dfull);
-              if (SB == 2 && n + 2 == t.count) umma_commit(aempty);
-            }
+          // tile g itself, as far as it could not be begun under the last one
+          if (!begun && !next_d()) { ok = false; break; }
+          if (SB == 1 && !with_x(g, ia % RA)) { ok = false; break; }
+          if (SB == 1 || !begun) next_done();
+          // the next one, where its resident operands can be there
+          begun = nt < p.nitems && (RA == 2 || nn > 0);
+          if (begun) {
+            if (!next_d()) { ok = false; break; }
+            if (SB == 2) next_done();
           }
+          const int s = g % RX;
           if (n == 0 && items > 0 && !mbar_wait(gempty, (items - 1) & 1)) { ok = false; break; }
           if (DV && !mbar_wait(&xfull[s], (g / RX) & 1)) { ok = false; break; }
           if (!mbar_wait(&pfull[g % SB], (g / SB) & 1)) { ok = false; break; }
           const uint32_t pa = tmem + C::kColS + (g % SB) * 128;
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 8; ++k) {
             umma_bf16_ta(tmem + C::kColX, pa + (k >> 2) * 64 + (k & 3) * 8, desc_at(xm, s * C::kTile + k * 2048), idx,
                          (n == 0 && k == 0) ? 0u : 1u);
-          umma_commit(&xempty[s]);
-          if (last) umma_commit(gfull);
+            if (k % (8 / HX) == 8 / HX - 1) umma_commit(&xempty[s * HX + k / (8 / HX)]);
+          }
+          if (n + 1 == t.count) umma_commit(gfull);
         }
         ++items;
       }
@@ -302,7 +333,7 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
     const uint32_t td = tq + C::kColD + half * 64;
     const float c2 = p.a.scale * 1.4426950408889634f;
     const int window = p.a.window, sinks = p.a.sinks;
-    // lse (log2) [128] and delta [128] of a tile's columns, as many as there are S buffers
+    // -lse (log2) [128] and -delta [128] of a tile's columns, as many as there are S buffers
     float* cols = reinterpret_cast<float*>(smem + C::kOffCol);
     const int mycol = threadIdx.x - 64;                          // 0..255
     int g = 0, ic = 0;
@@ -310,11 +341,11 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
     for (int item = blockIdx.x; ok && item < p.nitems; item += gridDim.x) {
       const BwdItem<MODE> t(p, item);
       const int mine = t.pos + r;                     // this row's position
-      float rl = 0.f, rd = 0.f;
+      float rl = 0.f, rd = 0.f;                       // -lse (log2), -delta
       if (MODE == WATTN_DQ && mine < t.len && t.a0 + r < p.a.Tq) {
         const int64_t at = (static_cast<int64_t>(t.b) * p.a.H + t.ha) * p.a.Tq + t.a0 + r;
-        rl = p.a.lse[at] * 1.4426950408889634f;
-        rd = p.a.delta[at];
+        rl = p.a.lse[at] * -1.4426950408889634f;
+        rd = -p.a.delta[at];
       }
       for (int n = 0; n < t.count; ++n, ++g) {
         const int t0 = t.at(n), b0 = t0 + half * 64;  // positions of the tile's and of this half's first column
@@ -326,7 +357,7 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
           const int i = t0 + (mycol & 127);
           if (i < t.hi && (MODE == WATTN_DK || mycol < 128)) {
             const int64_t at = (static_cast<int64_t>(t.b) * p.a.H + t.head(n)) * p.a.Tq + i - off;
-            x = mycol < 128 ? p.a.lse[at] * 1.4426950408889634f : p.a.delta[at];
+            x = mycol < 128 ? p.a.lse[at] * -1.4426950408889634f : -p.a.delta[at];
           }
         }
         float dp[64];
@@ -388,11 +419,16 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
               if (MODE == WATTN_DK)
                 asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(d4.x), "=f"(d4.y), "=f"(d4.z), "=f"(d4.w) : "r"(col_s + 512 + (c0 + c) * 4));
             }
-            const float ll[4] = {l4.x, l4.y, l4.z, l4.w}, dd[4] = {d4.x, d4.y, d4.z, d4.w};
+            const float2 ll[2] = {make_float2(l4.x, l4.y), make_float2(l4.z, l4.w)};
+            const float2 dd[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float pr = ex2_approx(fmaf(s[c + k], c2, -ll[k]));
-              s[c + k] = DV ? pr : pr * (dp[c0 + c + k] - dd[k]);
+            for (int k = 0; k < 4; k += 2) {
+              float2 e = fma_f32x2(make_float2(s[c + k], s[c + k + 1]), make_float2(c2, c2), ll[k / 2]);
+              e.x = ex2_approx(e.x);
+              e.y = ex2_approx(e.y);
+              if (!DV) e = mul_f32x2(e, add_f32x2(make_float2(dp[c0 + c + k], dp[c0 + c + k + 1]), dd[k / 2]));
+              s[c + k] = e.x;
+              s[c + k + 1] = e.y;
             }
           }
           if (!whole) {

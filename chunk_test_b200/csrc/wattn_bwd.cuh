@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
         if (MODE != WATTN_DQ && !mbar_wait_warp(cfull, g & 1)) { ok = false; break; }
         tc_fence_after();
         bool whole;
-        int clo, chi, csk;                            // columns c with clo < c <= chi, or csk's side
+        int clo, chi, csk;                            // columns c with clo < c <= chi, or c <= chi below csk
         if (MODE == WATTN_DQ) {
           whole = b0 + 63 <= t.pos && (b0 > t.pos + 127 - window || b0 + 63 < sinks) && t.pos + 127 < t.len;
           chi = mine < t.len ? mine - b0 : -1;
@@ -403,9 +403,15 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
           const int top = mine < sinks ? t.hi - 1 : min(t.hi - 1, mine + window - 1);
           chi = top - b0;
           clo = mine - 1 - b0;
-          csk = -1;
+          csk = 0;
         }
+        // a warp none of whose rows sees a column: a sink tile's other keys, or beside the diagonal
+        const bool none = !whole && __all_sync(0xffffffffu, chi < 0 || ((clo >= 63 || chi <= clo) && csk <= 0));
         uint32_t hw[32];
+        if (none) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) hw[c] = 0;
+        } else {
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 32) {
           float s[32];
@@ -432,13 +438,15 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
             }
           }
           if (!whole) {
+            const uint32_t see = visible_bits(clo, chi, csk, c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c0 + c > chi || (c0 + c <= clo && c0 + c >= csk)) s[c] = 0.f;
+              if (!(see >> c & 1)) s[c] = 0.f;
           }
           // the last product's operand: half a step, 2^-8 of each
 #pragma unroll
           for (int c = 0; c < 16; ++c) hw[c0 / 2 + c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
+        }
         }
         // over the first half of the 64 columns that this thread has read
         tmem_st16u(ts, hw);

@@ -110,6 +110,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Bits 0..31: the columns base + bit below `n`.
+__device__ __forceinline__ uint32_t bits_below(int n, int base) {
+  const int k = n - base;
+  return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
+}
+// The visible ones of columns base .. base + 31: lo < c <= hi, or c < sk.
+__device__ __forceinline__ uint32_t visible_bits(int lo, int hi, int sk, int base) {
+  return bits_below(hi + 1, base) & (~bits_below(lo + 1, base) | bits_below(sk, base));
+}
+
 // Shared-memory descriptors of one operand differ by their start address only.
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
@@ -362,8 +372,12 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
       if (!whole) {
         const int hi = i < t.len ? i - j0 : -1, lo = i - window - j0, sk = sinks - j0;
 #pragma unroll
-        for (int c = 0; c < N; ++c)
-          if (c > hi || (c <= lo && c >= sk)) sv[c] = -INFINITY;
+        for (int c0 = 0; c0 < N; c0 += 32) {
+          const uint32_t see = visible_bits(lo, hi, sk, c0);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!(see >> c & 1)) sv[c0 + c] = -INFINITY;
+        }
       }
       float b4[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll

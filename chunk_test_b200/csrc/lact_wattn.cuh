@@ -212,25 +212,27 @@ static WattnParams wattn_params(const WattnDims& D, float scale, const int32_t* 
   return a;
 }
 
-// 4-D bf16 map (channel, token, head, batch) of a view, 128-byte swizzle,
-// boxes of 64 channels x `rows` tokens; elements outside read as zero.
-static bool map_view(CUtensorMap* m, const View4& v, const Extent4& e, uint32_t rows) {
+// 4-D bf16 map (channel, token, head, batch) of a view, boxes of 64 channels
+// (128-byte swizzle) or 32 (64-byte swizzle) x `rows` tokens; elements outside
+// read as zero and are not written.
+static bool map_view(CUtensorMap* m, const View4& v, const Extent4& e, uint32_t rows, uint32_t channels = 64) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(e.d), static_cast<cuuint64_t>(e.T), static_cast<cuuint64_t>(e.H),
                         static_cast<cuuint64_t>(e.B)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(v.st) * 2, static_cast<cuuint64_t>(v.sh) * 2,
                            static_cast<cuuint64_t>(v.sb) * 2};
-  cuuint32_t box[4] = {64, rows, 1, 1}, es[4] = {1, 1, 1, 1};
+  cuuint32_t box[4] = {channels, rows, 1, 1}, es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            channels == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DP>
 static cudaError_t wattn_fwd_bf16(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
   using C = WattnCfg<DP>;
-  static_assert(C::kSmem * C::kCtas <= kMaxSmemPerBlock, "dynamic shared memory above the SM's limit");
+  // 228 KB an SM, 1 KB of it reserved for each CTA
+  static_assert((C::kSmem + 1024) * C::kCtas <= 228 * 1024, "dynamic shared memory above the SM's limit");
   static bool done[64] = {};
   const cudaError_t e = set_smem(k_wattn_fwd<DP>, C::kSmem, done);
   if (e != cudaSuccess) return e;
@@ -238,7 +240,8 @@ static cudaError_t wattn_fwd_bf16(const WattnDims& D, const WattnParams& a, cuda
   std::memset(&f, 0, sizeof(f));
   const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
   if (!map_view(&f.tmQ, a.q, eq, 128) || !map_view(&f.tmK, a.k, ek, 128) || !map_view(&f.tmV, a.v, ek, C::kVKeys) ||
-      !map_view(&f.tmK32, a.k, ek, 32) || !map_view(&f.tmV32, a.v, ek, 32))
+      !map_view(&f.tmK32, a.k, ek, 32) || !map_view(&f.tmV32, a.v, ek, 32) ||
+      !map_view(&f.tmO, a.out, eq, 32, 32))
     return cudaErrorInvalidValue;
   f.a = a;
   f.nb = static_cast<int>(cdiv(D.Tq, 128));

@@ -5,14 +5,17 @@
 // sinks and of its window with an online softmax.  Where the sinks end with at
 // most 32 keys of a tile, that tile is 32 keys wide in every step.  Roles:
 //   warp 0     TMA producer of the queries and keys (NS = 1: of the values too).
-//   warp 1     issues S_j = Q K_j^T (tcgen05, M = 128); NS = 1: and O += P_j V_j.
+//   warp 1     issues S_j = Q K_j^T and O += P_j V_j (tcgen05, M = 128), in the
+//              order S_(j+1), P_j V_j (NS = 2): S_(j+1) first, because the softmax
+//              that waits for it is as long as both products.  One thread; it
+//              waits and commits as little as the rings allow, each of which
+//              costs 50 to 100 clocks in which it feeds nothing.
 //   warps 2-5  softmax, one query row per thread; P_j goes back to TMEM in
 //              bf16, over S_j, and is the second product's A operand from
-//              there, so shared memory carries K, V and Q only.
+//              there, so shared memory carries K, V and Q only.  The output
+//              leaves through a staging tile and bulk tensor stores (16-byte
+//              stores of a row per thread took 6600 clocks a query tile at d 256).
 //   warp 6     (NS = 2) TMA producer of the values, in slots of 64 keys.
-//   warp 7     (NS = 2) issues O += P_j V_j.
-// One thread issues, and it waits and commits as little as the rings allow:
-// each costs 50 to 100 clocks in which it feeds nothing.
 // Head dims up to 128: two CTAs per SM with one score buffer each (NS = 1); one
 // CTA's products run under the other's exponentials.  Above: one CTA per SM
 // and two score buffers (NS = 2).
@@ -42,6 +45,14 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 // A wait made by a whole warp, with one outcome for all of its lanes.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+// 4-D tiled store from shared memory (bulk-group completion); clips at the tensor's ends
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], bf16: A's row r is lane r, two elements of K per column.
@@ -127,6 +138,7 @@ struct WattnFwdParams {
   CUtensorMap tmQ;          // [d, Tq, H, B], box {64, 128}
   CUtensorMap tmK, tmV;     // [d, T, Hkv, B], boxes {64, 128}, {64, kVKeys}
   CUtensorMap tmK32, tmV32; // the same, box {64, 32}: a narrow sink tile
+  CUtensorMap tmO;          // out, box {32, 32}, 64-byte swizzle
   WattnParams a;
   int nb, ntiles;           // 128-query tiles per head, in all
 };
@@ -158,7 +170,7 @@ struct WattnCfg {
   static_assert(D % 64 == 0 && D >= 64 && D <= 256, "padded head dim");
   static constexpr int kNS = D <= 128 ? 1 : 2;            // score buffers
   static constexpr int kCtas = D <= 128 ? 2 : 1;          // CTAs per SM
-  static constexpr int kThreads = kNS == 1 ? 192 : 256;
+  static constexpr int kThreads = kNS == 1 ? 192 : 224;
   static constexpr int kKb = D / 64;
   static constexpr int kQBytes = kKb * 16384;
   // key slots of 128 keys x kKBlk 64-channel blocks, value slots of kVKeys keys
@@ -166,11 +178,13 @@ struct WattnCfg {
   static constexpr int kVKeys = kNS == 1 ? 128 : 64, kVPer = 128 / kVKeys;
   static constexpr int kVBox = kVKeys * 128;              // bytes of one box {64, kVKeys}
   static constexpr int kKSlot = kKBlk * 16384, kVSlot = kKb * kVBox;
-  static constexpr int kKR = D == 128 ? 1 : 2, kVR = D == 128 ? 1 : D == 64 ? 2 : 3;
-  static constexpr int kOffK = kQBytes, kOffV = kOffK + kKR * kKSlot, kOffBar = kOffV + kVR * kVSlot;
-  // qfull qempty | kfull[] kempty[] | vfull[] vempty[] | sfull[NS] pfull[NS] pvdone[NS] | ofull oempty
-  static constexpr int kBars = 2 + 2 * kKR + 2 * kVR + 3 * kNS + 2;
-  static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
+  static constexpr int kKR = D == 128 ? 1 : 2, kVR = D == 128 ? 1 : 2;
+  static constexpr int kOffK = kQBytes, kOffV = kOffK + kKR * kKSlot, kOffStage = kOffV + kVR * kVSlot;
+  static constexpr int kStages = kNS == 1 ? 2 : 4;        // staging tiles of a softmax warp: 32 rows x 32 channels
+  static constexpr int kOffBar = kOffStage + 4 * kStages * 2048;
+  // qfull qempty | kfull[] kempty[] | vfull[] vempty[] | sfull[NS] pfull[NS] | pvdone ofull oempty
+  static constexpr int kBars = 2 + 2 * kKR + 2 * kVR + 2 * kNS + 3;
+  static constexpr int kSmem = kOffBar + kBars * 8 + 16;
   static constexpr uint32_t kColO = 0, kColS = kNS == 1 ? 128 : 256, kCols = kNS == 1 ? 256 : 512;
 };
 
@@ -179,17 +193,23 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
     k_wattn_fwd(const __grid_constant__ WattnFwdParams p) {
   using C = WattnCfg<D>;
   constexpr int NS = C::kNS, KR = C::kKR, VR = C::kVR;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // The swizzled tiles want 1024-byte alignment.  Without static shared memory the
+  // dynamic part starts on it; it is checked below, since two CTAs leave no room
+  // to round up.
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t *qfull = bar, *qempty = bar + 1, *kfull = bar + 2, *kempty = kfull + KR, *vfull = kempty + KR,
            *vempty = vfull + VR, *sfull = vempty + VR, *pfull = sfull + NS, *pvdone = pfull + NS,
-           *ofull = pvdone + NS, *oempty = ofull + 1;
+           *ofull = pvdone + 1, *oempty = ofull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + C::kBars);
 
   griddep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (__syncthreads_or(*reinterpret_cast<volatile int*>(&g_status))) return;   // an earlier wait gave up
+  if (smem_u32(smem) & 1023) {
+    if (threadIdx.x == 0) atomicExch(&g_status, kStatusTimeout);
+    return;
+  }
   if (threadIdx.x == 0) {
     mbar_init(qfull, 1);
     mbar_init(qempty, 1);
@@ -204,8 +224,8 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
-      mbar_init(&pvdone[i], 1);
     }
+    mbar_init(pvdone, 1);
     mbar_init(ofull, 1);
     mbar_init(oempty, 4);
     fence_barrier_init();
@@ -261,7 +281,7 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
         }
       }
     }
-  } else if (warp == 1 || warp == 7) {
+  } else if (warp == 1) {
     // ---------------------------------------------------------- products
     if (lane == 0) {
       const uint32_t sbase = smem_u32(smem);
@@ -303,45 +323,27 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
                            ido, (first && vs == 0 && k == 0) ? 0u : 1u);
           umma_commit(&vempty[s]);
         }
-        if (NS == 2) umma_commit(&pvdone[pc % NS]);
+        if (NS == 2) umma_commit(pvdone);
         if (last) umma_commit(ofull);
         return true;
       };
       int sc = 0, pc = 0, tc = 0;
       bool ok = true;
-      if constexpr (NS == 2) {
-        for (int tile = blockIdx.x; ok && tile < p.ntiles; tile += gridDim.x) {
-          const QueryTile t(p.a, p.nb, tile);
-          if (t.count == 0) continue;
-          if (warp == 1) {
-            if (!mbar_wait(qfull, tc & 1)) break;
-            for (int n = 0; ok && n < t.count; ++n, ++sc) {
-              // P of two tiles ago, in this buffer, has been used
-              if (sc >= 2 && !mbar_wait(&pvdone[sc & 1], ((sc >> 1) - 1) & 1)) { ok = false; break; }
-              ok = scores(sc, n == t.narrow);
-            }
-            if (ok) umma_commit(qempty);
-          } else {
-            if (tc > 0 && !mbar_wait(oempty, (tc - 1) & 1)) break;
-            for (int n = 0; ok && n < t.count; ++n, ++pc) ok = output(pc, n == t.narrow, n == 0, n + 1 == t.count);
-          }
-          ++tc;
+      for (int tile = blockIdx.x; ok && tile < p.ntiles; tile += gridDim.x) {
+        const QueryTile t(p.a, p.nb, tile);
+        if (t.count == 0) continue;
+        if (!mbar_wait(qfull, tc & 1) || !scores(sc++, t.narrow == 0)) break;
+        if (t.count == 1) umma_commit(qempty);
+        for (int n = 0; ok && n < t.count; ++n, ++pc) {
+          // S of the next key tile.  NS = 2: ahead of this one's product, over the P
+          // of the last; NS = 1: behind it, over this P.  In order, so nothing waits.
+          if (NS == 2 && n + 1 < t.count) ok = scores(sc++, n + 1 == t.narrow);
+          if (ok && n == 0 && tc > 0 && !mbar_wait(oempty, (tc - 1) & 1)) ok = false;
+          ok = ok && output(pc, n == t.narrow, n == 0, n + 1 == t.count);
+          if (NS == 1 && ok && n + 1 < t.count) ok = scores(sc++, n + 1 == t.narrow);
+          if (ok && n + 2 == t.count) umma_commit(qempty);
         }
-      } else {
-        for (int tile = blockIdx.x; ok && tile < p.ntiles; tile += gridDim.x) {
-          const QueryTile t(p.a, p.nb, tile);
-          if (t.count == 0) continue;
-          if (!mbar_wait(qfull, tc & 1) || !scores(sc++, t.narrow == 0)) break;
-          if (t.count == 1) umma_commit(qempty);
-          for (int n = 0; ok && n < t.count; ++n, ++pc) {
-            if (n == 0 && tc > 0 && !mbar_wait(oempty, (tc - 1) & 1)) { ok = false; break; }
-            // S of the next tile goes over P: issued behind the product that reads it
-            ok = output(pc, n == t.narrow, n == 0, n + 1 == t.count) &&
-                 (n + 1 == t.count || scores(sc++, n + 1 == t.narrow));
-            if (ok && n + 2 == t.count) umma_commit(qempty);
-          }
-          ++tc;
-        }
+        ++tc;
       }
     }
   } else {
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
     const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float c2 = p.a.scale * 1.4426950408889634f;
     const int window = p.a.window, sinks = p.a.sinks;
-    int sc = 0, iv = 0, tc = 0;
+    int sc = 0, iv = 0, tc = 0, nst = 0;
     bool ok = true;
     float mx, sum;
     // one key tile of N columns; false where a wait gave up
@@ -364,27 +366,36 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
       if (!mbar_wait_warp(&sfull[sb], (sc / NS) & 1)) return false;
       tc_fence_after();
       const uint32_t ts = tq + C::kColS + sb * 128;
-      float sv[N];
-#pragma unroll
-      for (int c0 = 0; c0 < N; c0 += 32) tmem_ld32(ts + c0, sv + c0);
-      tmem_ld_wait();
       const bool whole = j0 + N - 1 <= t.i0 && (j0 > last - window || j0 + N - 1 < sinks) && last < t.len;
-      if (!whole) {
-        const int hi = i < t.len ? i - j0 : -1, lo = i - window - j0, sk = sinks - j0;
+      const int hi = i < t.len ? i - j0 : -1, lo = i - window - j0, sk = sinks - j0;
+      // scores of columns [c0, c0 + W), the others' at -inf
+      auto load = [&](float* sv, int c0, auto width) {
+        constexpr int W = decltype(width)::value;
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 32) {
-          const uint32_t see = visible_bits(lo, hi, sk, c0);
+        for (int c = 0; c < W; c += 32) tmem_ld32(ts + c0 + c, sv + c);
+        tmem_ld_wait();
+        if (!whole) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (!(see >> c & 1)) sv[c0 + c] = -INFINITY;
+          for (int w = 0; w < W; w += 32) {
+            const uint32_t see = visible_bits(lo, hi, sk, c0 + w);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(see >> c & 1)) sv[w + c] = -INFINITY;
+          }
         }
-      }
-      float b4[4] = {sv[0], sv[1], sv[2], sv[3]};
+      };
+      // The upper half is loaded twice, for the maximum and for the exponentials:
+      // a row of 128 scores in registers spills where two CTAs share an SM.
+      constexpr int W = N < 64 ? N : 64;
+      using Width = std::integral_constant<int, W>;
+      float sv[W], b4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 4; c < N; c += 8) {
-        b4[0] = max3(b4[0], sv[c], sv[c + 1]);
-        b4[1] = max3(b4[1], sv[c + 2], sv[c + 3]);
-        if (c + 4 < N) {
+      for (int c0 = N - W; c0 >= 0; c0 -= W) {
+        load(sv, c0, Width());
+#pragma unroll
+        for (int c = 0; c < W; c += 8) {
+          b4[0] = max3(b4[0], sv[c], sv[c + 1]);
+          b4[1] = max3(b4[1], sv[c + 2], sv[c + 3]);
           b4[2] = max3(b4[2], sv[c + 4], sv[c + 5]);
           b4[3] = max3(b4[3], sv[c + 6], sv[c + 7]);
         }
@@ -401,7 +412,7 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
       }
       if (__any_sync(0xffffffffu, grow)) {
         // NS = 1: S_n came behind the last product; NS = 2: wait for it
-        if (NS == 2 && !mbar_wait_warp(&pvdone[(sc - 1) & 1], ((sc - 1) >> 1) & 1)) return false;
+        if (NS == 2 && !mbar_wait_warp(pvdone, (sc - 1) & 1)) return false;
         tc_fence_after();
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 16) {
@@ -418,18 +429,22 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
       const float off = mx == -INFINITY ? 0.f : -mx * c2;
       float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c0 = 0; c0 < N; c0 += 32) {
-        uint32_t hw[16];
+      for (int c0 = 0; c0 < N; c0 += W) {
+        if (c0 > 0) load(sv, c0, Width());
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float2 e = fma_f32x2(make_float2(sv[c0 + 2 * c], sv[c0 + 2 * c + 1]), make_float2(c2, c2),
-                               make_float2(off, off));
-          e.x = ex2_approx(e.x);
-          e.y = ex2_approx(e.y);
-          ps[c & 1] = add_f32x2(ps[c & 1], e);
-          hw[c] = pack_bf16x2(e.x, e.y);   // the second product's operand: half a step, 2^-8 of each
+        for (int w = 0; w < W; w += 32) {
+          uint32_t hw[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float2 e = fma_f32x2(make_float2(sv[w + 2 * c], sv[w + 2 * c + 1]), make_float2(c2, c2),
+                                 make_float2(off, off));
+            e.x = ex2_approx(e.x);
+            e.y = ex2_approx(e.y);
+            ps[c & 1] = add_f32x2(ps[c & 1], e);
+            hw[c] = pack_bf16x2(e.x, e.y);   // the second product's operand: half a step, 2^-8 of each
+          }
+          tmem_st16u(ts + (c0 + w) / 2, hw);
         }
-        tmem_st16u(ts + c0 / 2, hw);
       }
       sum += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
       // value rows behind the sequence: a probability of 0 times whatever is there must stay 0
@@ -466,35 +481,47 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
       if (in)
         p.a.lse[(static_cast<int64_t>(t.b) * p.a.H + t.h) * p.a.Tq + t.q0 + r] =
             some ? fmaf(mx, p.a.scale, logf(sum)) : -INFINITY;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.out.p) + t.b * p.a.out.sb + t.h * p.a.out.sh +
-                           static_cast<int64_t>(t.q0 + r) * p.a.out.st;
-      if (t.count == 0) {
-        if (in)
-          for (int c = 0; c < p.a.d; c += 8) st_global_v4(dst + c, 0, 0, 0, 0);
-        continue;
+      if (t.count > 0) {
+        if (!mbar_wait_warp(ofull, tc & 1)) break;
+        ++tc;
+        tc_fence_after();
       }
-      if (!mbar_wait_warp(ofull, tc & 1)) break;
-      ++tc;
-      tc_fence_after();
+      // rows of 64 bytes in 64-byte swizzle; rows and channels outside are clipped by the store
+      const uint32_t stage = smem_u32(smem + C::kOffStage) + (warp - 2) * C::kStages * 2048;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
+      for (int c0 = 0; c0 < p.a.d; c0 += 32, ++nst) {
         float o[32];
+        if (t.count > 0) {
+          __syncwarp();
+          tmem_ld32(tq + C::kColO + c0, o);
+          tmem_ld_wait();
+        }
+        const uint32_t to = stage + (nst % C::kStages) * 2048;
+        if (lane == 0) {   // the store that last read this staging tile is done with it
+          asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(C::kStages - 1) : "memory");
+        }
         __syncwarp();
-        tmem_ld32(tq + C::kColO + c0, o);
-        tmem_ld_wait();
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if (in && c0 + 8 * g < p.a.d) {
+        for (int g = 0; g < 4; ++g) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) o[8 * g + c] = some ? o[8 * g + c] * inv : 0.f;
-            st_global_v4(dst + c0 + 8 * g, pack_bf16x2(o[8 * g], o[8 * g + 1]), pack_bf16x2(o[8 * g + 2], o[8 * g + 3]),
-                         pack_bf16x2(o[8 * g + 4], o[8 * g + 5]), pack_bf16x2(o[8 * g + 6], o[8 * g + 7]));
-          }
+          for (int c = 8 * g; c < 8 * g + 8; ++c) o[c] = some ? o[c] * inv : 0.f;
+          st_shared_v4(to + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(o[8 * g], o[8 * g + 1]),
+                       pack_bf16x2(o[8 * g + 2], o[8 * g + 3]), pack_bf16x2(o[8 * g + 4], o[8 * g + 5]),
+                       pack_bf16x2(o[8 * g + 6], o[8 * g + 7]));
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && t.q0 + quarter * 32 < p.a.Tq) {
+          tma_store_4d(&p.tmO, to, c0, t.q0 + quarter * 32, t.h, t.b);
+          bulk_commit_group();
+        }
       }
+      if (t.count == 0) continue;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(oempty);
     }
+    if (lane == 0) bulk_wait_all();   // the last stores, before the shared memory goes
   }
   tc_fence_before();
   cta_sync_converged();

@@ -293,7 +293,7 @@ static cudaError_t wattn_bwd_bf16(const WattnDims& D, const WattnParams& a, cuda
   CUtensorMap *k = MODE == WATTN_DQ ? &f.tmB1 : &f.tmA1, *v = MODE == WATTN_DQ ? &f.tmB2 : &f.tmA2;
   if (!map_view(q, a.q, eq, 128) || !map_view(g, a.dout, eq, 128) || !map_view(k, a.k, ek, 128) ||
       !map_view(v, a.v, ek, 128) ||
-      !(MODE == WATTN_DQ ? map_view(&f.tmX64, a.k, ek, 64) : map_view(&f.tmX64, MODE == WATTN_DK ? a.q : a.dout, eq, 64)))
+      !(MODE == WATTN_DQ ? map_view(&f.tmX64, a.k, ek, 64) : map_view(&f.tmX64, MODE == WATTN_DV ? a.dout : a.q, eq, 64)))
     return cudaErrorInvalidValue;
   f.a = a;
   f.sink_tiles = D.sink_tiles;
@@ -350,8 +350,13 @@ static void wattn_bwd_run(const WattnDims& D, const WattnParams& a, cudaStream_t
   if (D.dtype == LACT_F32) {
     L(K_WATTN_DKV, [&]() -> cudaError_t { LACT_BY_DP(D.DP, wattn_dkv_f32<DP>(D, a, st)) });
   } else {
-    L(K_WATTN_DKV, [&]() -> cudaError_t { LACT_BY_DP(D.DP, (wattn_bwd_bf16<DP, WATTN_DK>(D, a, st))) });
-    L(K_WATTN_DKV, [&]() -> cudaError_t { LACT_BY_DP(D.DP, (wattn_bwd_bf16<DP, WATTN_DV>(D, a, st))) });
+    // both in one pass where TMEM holds both accumulators beside S and dP
+    if (D.DP <= 128) {
+      L(K_WATTN_DKV, [&] { return D.DP == 64 ? wattn_bwd_bf16<64, WATTN_DKV>(D, a, st) : wattn_bwd_bf16<128, WATTN_DKV>(D, a, st); });
+    } else {
+      L(K_WATTN_DKV, [&] { return D.DP == 192 ? wattn_bwd_bf16<192, WATTN_DK>(D, a, st) : wattn_bwd_bf16<256, WATTN_DK>(D, a, st); });
+      L(K_WATTN_DKV, [&] { return D.DP == 192 ? wattn_bwd_bf16<192, WATTN_DV>(D, a, st) : wattn_bwd_bf16<256, WATTN_DV>(D, a, st); });
+    }
   }
   if (D.sink_tiles > 0) L(K_WATTN_ELEM, [&] { return launch_wattn_sums(D, a, st); });
 }

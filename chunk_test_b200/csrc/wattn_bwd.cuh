@@ -31,7 +31,7 @@
 
 namespace lact {
 
-enum WattnMode { WATTN_DQ, WATTN_DK, WATTN_DV };
+enum WattnMode { WATTN_DQ, WATTN_DK, WATTN_DV, WATTN_DKV };   // DKV: d <= 128
 
 struct WattnBwdParams {
   CUtensorMap tmA1, tmA2;   // q, dout (dQ) or k, v (dK, dV), box {64, 128}
@@ -93,8 +93,10 @@ template <int D, int MODE>
 struct BwdCfg {
   static constexpr int kKb = D / 64;
   static constexpr bool kDv = MODE == WATTN_DV;
-  static constexpr int kSB = kDv || D <= 128 ? 2 : 1;      // buffers of S (and of dS or P, which go over it)
-  static constexpr int kCol = kDv ? 128 : MODE == WATTN_DK ? 256 : 0;   // lse and delta of a tile's columns
+  static constexpr bool kBoth = MODE == WATTN_DKV;
+  static_assert(!kBoth || D <= 128, "both accumulators beside S and dP");
+  static constexpr int kSB = kDv || (D <= 128 && !kBoth) ? 2 : 1;      // buffers of S (and of dS or P, which go over it)
+  static constexpr int kCol = kDv ? 128 : MODE != WATTN_DQ ? 256 : 0;   // lse and delta of a tile's columns
   static constexpr int kABytes = kKb * 16384;
   static constexpr int kAll = kDv ? kABytes : 2 * kABytes;
   // two sets of resident operands where they fit: the next item's first tile is
@@ -103,29 +105,29 @@ struct BwdCfg {
   static constexpr int kTile = kKb * 16384;                // a B tile of 128 rows
   // The operand of the last product (B1; dV: B2) stays until that product is
   // done: whole tiles.  The other one is K-major only and goes by blocks of 64
-  // channels.
+  // channels (DKV: it is an operand of dV too, and its blocks stay as well).
   static constexpr int kBlocks = (230400 - kSB * kCol * 4 - kRA * kAll) / 16384;  // 16 KB blocks there is room for
   static constexpr int kRx = kBlocks >= 3 * kKb + 2 ? 3 : kBlocks >= 2 * kKb + 2 ? 2 : 1;
   // a single X slot is refilled by halves of 64 rows: the product that reads it
   // is done with the first half before the second
   static constexpr int kHx = kRx == 1 ? 2 : 1;
   static constexpr int kRy0 = kBlocks - kRx * kKb, kRy = kRy0 > 2 * kKb ? 2 * kKb : kRy0;
-  static_assert(kRy >= 2, "room for two blocks");
+  static_assert(kRy >= 2 && (!kBoth || kRy == 2 * kKb), "room for two blocks (DKV: tiles)");
   static constexpr int kOffX = kRA * kAll, kOffY = kOffX + kRx * kTile, kOffCol = kOffY + kRy * 16384;
   static constexpr int kOffBar = kOffCol + kSB * kCol * 4;
   // afull[RA] aempty[RA] | xfull[] xempty[] | yfull[] yempty[] | sfull[SB] pfull[SB] dfull dread cfull | gfull gempty
   static constexpr int kBars = 2 * kRA + kRx + kRx * kHx + 2 * kRy + 2 * kSB + 3 + 2;
   static constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
   static constexpr int kThreads = 352;
-  // columns: the accumulator, S, dP (dV has none)
-  static constexpr uint32_t kColX = 0, kColS = 256, kColD = kSB == 2 ? 128 : 384;
+  // columns: the accumulator (DKV: dK), DKV's dV, S, dP (dV has none)
+  static constexpr uint32_t kColX = 0, kColV = 128, kColS = 256, kColD = kSB == 2 ? 128 : 384;
 };
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ WattnBwdParams p) {
   using C = BwdCfg<D, MODE>;
   constexpr int RX = C::kRx, RY = C::kRy, KB = C::kKb, SB = C::kSB, RA = C::kRA, HX = C::kHx;
-  constexpr bool DV = C::kDv;
+  constexpr bool DV = C::kDv, BOTH = C::kBoth;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -230,7 +232,8 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
       const uint64_t a1 = smem_desc_sw128(sbase, 16u, 1024u), a2 = smem_desc_sw128(sbase + C::kABytes, 16u, 1024u),
                      xk = smem_desc_sw128(sbase + C::kOffX, 16u, 1024u),
                      xm = smem_desc_sw128(sbase + C::kOffX, 16384u, 1024u),
-                     yk = smem_desc_sw128(sbase + C::kOffY, 16u, 1024u);
+                     yk = smem_desc_sw128(sbase + C::kOffY, 16u, 1024u),
+                     ym = smem_desc_sw128(sbase + C::kOffY, 16384u, 1024u);
       int iy = 0;
       // S of tile h in all, with the tile X(h) (dV: with Y)
       auto with_x = [&](int h, int abuf) -> bool {
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
           for (int k = 0; k < 4; ++k)
             umma_bf16(d, desc_at(a, abuf * C::kAll + kb * 16384 + k * 32), desc_at(yk, s * 16384 + k * 32), ids,
                       (kb | k) ? 1u : 0u);
-          umma_commit(&yempty[s]);
+          if (!BOTH) umma_commit(&yempty[s]);
         }
         return true;
       };
@@ -316,9 +319,15 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
           const uint32_t pa = tmem + C::kColS + (g % SB) * 128;
           tc_fence_after();
 #pragma unroll
+          for (int k = 0; BOTH && k < 8; ++k)   // P: columns 0..15 of each 32, dS: 16..31
+            umma_bf16_ta(tmem + C::kColV, pa + (k >> 1) * 32 + (k & 1) * 8,
+                         desc_at(ym, (g % (RY / KB)) * C::kTile + k * 2048), idx, (n == 0 && k == 0) ? 0u : 1u);
+          if (BOTH)
+            for (int kb = 0; kb < KB; ++kb) umma_commit(&yempty[(g % (RY / KB)) * KB + kb]);
+#pragma unroll
           for (int k = 0; k < 8; ++k) {
-            umma_bf16_ta(tmem + C::kColX, pa + (k >> 2) * 64 + (k & 3) * 8, desc_at(xm, s * C::kTile + k * 2048), idx,
-                         (n == 0 && k == 0) ? 0u : 1u);
+            umma_bf16_ta(tmem + C::kColX, pa + (BOTH ? (k >> 1) * 32 + 16 + (k & 1) * 8 : (k >> 2) * 64 + (k & 3) * 8),
+                         desc_at(xm, s * C::kTile + k * 2048), idx, (n == 0 && k == 0) ? 0u : 1u);
             if (k % (8 / HX) == 8 / HX - 1) umma_commit(&xempty[s * HX + k / (8 / HX)]);
           }
           if (n + 1 == t.count) umma_commit(gfull);
@@ -355,18 +364,20 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
         if (MODE != WATTN_DQ) {
           // the columns' statistics: one value per thread
           const int i = t0 + (mycol & 127);
-          if (i < t.hi && (MODE == WATTN_DK || mycol < 128)) {
+          if (i < t.hi && (!DV || mycol < 128)) {
             const int64_t at = (static_cast<int64_t>(t.b) * p.a.H + t.head(n)) * p.a.Tq + i - off;
             x = mycol < 128 ? p.a.lse[at] * -1.4426950408889634f : -p.a.delta[at];
           }
         }
-        float dp[64];
-        if (!DV) {
+        float dp[BOTH ? 32 : 64];
+        if (BOTH) {
+          if (!mbar_wait_warp(dfull, g & 1)) { ok = false; break; }
+        } else if (!DV) {
           // dP first, so that its buffer is free while dS is computed
           if (!mbar_wait_warp(dfull, g & 1)) { ok = false; break; }
           tc_fence_after();
           tmem_ld32(td, dp);
-          tmem_ld32(td + 32, dp + 32);
+          tmem_ld32(td + 32, dp + (BOTH ? 0 : 32));
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
@@ -385,7 +396,11 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
           if (!mbar_wait_warp(&xfull[s], (g / RX) & 1)) { ok = false; break; }
           const uint32_t xb = smem_u32(smem) + C::kOffX + s * C::kTile;
           for (int e = keep * 8 + mycol; e < 1024; e += 256)
-            for (int kb = 0; kb < KB; ++kb) st_shared_v4(xb + kb * 16384 + e * 16, 0, 0, 0, 0);
+            for (int kb = 0; kb < KB; ++kb) {
+              st_shared_v4(xb + kb * 16384 + e * 16, 0, 0, 0, 0);
+              if (BOTH)   // Y's blocks are there: dP has been formed from them
+                st_shared_v4(smem_u32(smem) + C::kOffY + (g % (RY / KB)) * C::kTile + kb * 16384 + e * 16, 0, 0, 0, 0);
+            }
           fence_async_smem();
         }
         if (MODE != WATTN_DQ && !mbar_wait_warp(cfull, g & 1)) { ok = false; break; }
@@ -411,18 +426,32 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
         if (none) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) hw[c] = 0;
+          if (BOTH) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dread);
+            tmem_st16u(ts, hw);
+            tmem_st16u(ts + 16, hw);
+            tmem_st16u(ts + 32, hw);
+            tmem_st16u(ts + 48, hw);
+          }
         } else {
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 32) {
           float s[32];
           tmem_ld32(ts + c0, s);
+          if (BOTH) tmem_ld32(td + c0, dp);
           tmem_ld_wait();
+          if (BOTH && c0 == 32) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dread);
+          }
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
             float4 l4 = make_float4(rl, rl, rl, rl), d4 = make_float4(rd, rd, rd, rd);
             if (MODE != WATTN_DQ) {
               asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(l4.x), "=f"(l4.y), "=f"(l4.z), "=f"(l4.w) : "r"(col_s + (c0 + c) * 4));
-              if (MODE == WATTN_DK)
+              if (!DV)
                 asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(d4.x), "=f"(d4.y), "=f"(d4.z), "=f"(d4.w) : "r"(col_s + 512 + (c0 + c) * 4));
             }
             const float2 ll[2] = {make_float2(l4.x, l4.y), make_float2(l4.z, l4.w)};
@@ -432,54 +461,72 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
               float2 e = fma_f32x2(make_float2(s[c + k], s[c + k + 1]), make_float2(c2, c2), ll[k / 2]);
               e.x = ex2_approx(e.x);
               e.y = ex2_approx(e.y);
-              if (!DV) e = mul_f32x2(e, add_f32x2(make_float2(dp[c0 + c + k], dp[c0 + c + k + 1]), dd[k / 2]));
-              s[c + k] = e.x;
-              s[c + k + 1] = e.y;
+              const int d = (BOTH ? 0 : c0) + c + k;
+              if (BOTH) {
+                s[c + k] = e.x;
+                s[c + k + 1] = e.y;
+              }
+              if (!DV) e = mul_f32x2(e, add_f32x2(make_float2(dp[d], dp[d + 1]), dd[k / 2]));
+              (BOTH ? dp : s)[c + k] = e.x;
+              (BOTH ? dp : s)[c + k + 1] = e.y;
             }
           }
           if (!whole) {
             const uint32_t see = visible_bits(clo, chi, csk, c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (!(see >> c & 1)) s[c] = 0.f;
+              if (!(see >> c & 1)) {
+                s[c] = 0.f;
+                if (BOTH) dp[c] = 0.f;
+              }
           }
           // the last product's operand: half a step, 2^-8 of each
 #pragma unroll
-          for (int c = 0; c < 16; ++c) hw[c0 / 2 + c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
+          for (int c = 0; c < 16; ++c) {
+            hw[(BOTH ? 0 : c0 / 2) + c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
+            if (BOTH) hw[16 + c] = pack_bf16x2(dp[2 * c], dp[2 * c + 1]);
+          }
+          if (BOTH) {   // P and dS over the 32 columns that this thread has read
+            tmem_st16u(ts + c0, hw);
+            tmem_st16u(ts + c0 + 16, hw + 16);
+          }
         }
         }
         // over the first half of the 64 columns that this thread has read
-        tmem_st16u(ts, hw);
-        tmem_st16u(ts + 16, hw + 16);
+        if (!BOTH) {
+          tmem_st16u(ts, hw);
+          tmem_st16u(ts + 16, hw + 16);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[g % SB]);
       }
       if (!ok) break;
-      // the gradient's rows: this half of the channels
+      // the gradient's rows: this half of the channels (DKV: the first half dK, the second dV)
       if (t.count > 0) {
         if (!mbar_wait_warp(gfull, ic & 1)) break;
         ++ic;
         tc_fence_after();
       }
-      const float mul = DV ? 1.0f : p.a.scale;
+      const bool is_v = DV || (BOTH && half == 1);
+      const float mul = is_v ? 1.0f : p.a.scale;
       const int row = t.a0 + r;
       const bool in = row < (MODE == WATTN_DQ ? p.a.Tq : p.a.T);
       const bool zero = t.count == 0 || (MODE == WATTN_DQ && mine >= t.len);
-      const View4& o = MODE == WATTN_DQ ? p.a.dq : MODE == WATTN_DK ? p.a.dk : p.a.dv;
+      const View4& o = MODE == WATTN_DQ ? p.a.dq : is_v ? p.a.dv : p.a.dk;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.p) + t.b * o.sb + t.ha * o.sh + static_cast<int64_t>(row) * o.st;
       const bool partial = MODE != WATTN_DQ && t.kt < p.sink_tiles;
       float* pd = nullptr;
       if (partial)
         pd = p.a.part + ((((static_cast<int64_t>(t.b) * p.a.Hkv + t.ha) * p.sink_tiles + t.kt) * p.parts + t.part) * 2 +
-                         (DV ? 1 : 0)) * (128 * D) + r * D;
+                         (is_v ? 1 : 0)) * (128 * D) + r * D;
 #pragma unroll 1
-      for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+      for (int c0 = BOTH ? 0 : half * (D / 2); c0 < (BOTH ? D : (half + 1) * (D / 2)); c0 += 32) {
         float x[32];
         if (t.count > 0) {
           __syncwarp();
-          tmem_ld32(tq + C::kColX + c0, x);
+          tmem_ld32(tq + (BOTH && is_v ? C::kColV : C::kColX) + c0, x);
           tmem_ld_wait();
         }
 #pragma unroll

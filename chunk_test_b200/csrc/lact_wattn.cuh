@@ -160,6 +160,7 @@ static RotaryParams rotary_params(const lact_rotary_problem* p, const RotaryDims
 
 // ------------------------------------------------------------------ window attention
 constexpr int kWattnFarRows = 1024;   // query rows of a sink tile's far part
+constexpr int kFewRounds = 8;         // rounds of persistent CTAs below which the short tiles go last
 
 struct WattnDims {
   int64_t B, H, Hkv, T, Tq, d, DP;
@@ -248,6 +249,7 @@ static cudaError_t wattn_fwd_bf16(const WattnDims& D, const WattnParams& a, cuda
   const int64_t tiles = D.B * D.H * f.nb;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   f.ntiles = static_cast<int>(tiles);
+  f.a.heads_first = tiles < kFewRounds * sm_count() * C::kCtas;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tiles, sm_count() * C::kCtas)));
   return launch_pdl(k_wattn_fwd<DP>, grid, dim3(C::kThreads), C::kSmem, st, f);
 }
@@ -302,6 +304,7 @@ static cudaError_t wattn_bwd_bf16(const WattnDims& D, const WattnParams& a, cuda
   const int64_t items = D.B * (MODE == WATTN_DQ ? D.H : D.Hkv) * f.per_head;
   if (items > INT32_MAX) return cudaErrorInvalidValue;
   f.nitems = static_cast<int>(items);
+  f.a.heads_first = items < kFewRounds * sm_count();
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(items, sm_count())));
   return launch_pdl(k_wattn_bwd<DP, MODE>, grid, dim3(C::kThreads), C::kSmem, st, f);
 }

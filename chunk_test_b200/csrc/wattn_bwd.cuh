@@ -53,12 +53,12 @@ struct BwdItem {
   int kt, part;
   __device__ __forceinline__ BwdItem(const WattnBwdParams& q, int item) {
     const WattnParams& p = q.a;
-    const int x = item % q.per_head, ba = item / q.per_head;
     if (MODE == WATTN_DQ) {
-      b = ba / p.H;
-      ha = ba % p.H;
+      const TileAt at = query_tile_at(p, q.per_head, item);
+      b = at.b;
+      ha = at.h;
       hb0 = ha / p.group;
-      a0 = x * 128;
+      a0 = at.m * 128;
       pos = a0 + p.T - p.Tq;
       len = seq_len(p, b);
       const int last = min(min(pos + 128, p.T), len) - 1;
@@ -66,8 +66,10 @@ struct BwdItem {
       sink_tiles = min((p.sinks + 127) >> 7, first);
       count = pos < len ? sink_tiles + (last >> 7) - first + 1 : 0;
     } else {
-      b = ba / p.Hkv;
-      ha = ba % p.Hkv;
+      // all key heads at one tile together, the last tiles, which fewer queries see, last
+      const int heads = p.B * p.Hkv, x = item / heads;
+      b = item % heads / p.Hkv;
+      ha = item % p.Hkv;
       hb0 = ha * p.group;
       const int split = q.sink_tiles * q.parts;
       kt = x < split ? x / q.parts : x - split + q.sink_tiles;

@@ -24,10 +24,44 @@ struct WattnParams {
   int B, H, Hkv, group, T, Tq, d;    // group = H / Hkv
   int window, sinks;                 // each at most T
   int far_rows;                      // query rows of one far part of a sink tile
+  int heads_first;                   // order of the query tiles (query_tile_at)
 };
 
 __device__ __forceinline__ int seq_len(const WattnParams& p, int b) {
   return p.lengths ? max(0, min(p.lengths[b], p.T)) : p.T;
+}
+
+// The v-th query tile of 128 rows in the order in which persistent CTAs take
+// them: first the tiles that hold tokens, then the tiles behind the lengths,
+// which are only filled; the later positions of a sequence first (the first
+// window's tiles see fewer keys).  heads_first: all heads at one position
+// together, so that those short tiles make the last round: for few rounds (the
+// dQ of 768 tiles on 148 SMs: 324 us, 362 head by head).  Else head by head, whose
+// CTAs share keys in L2 (the forward of 3072 tiles: 718 us, 752 the other way).
+struct TileAt {
+  int b, h, m;
+};
+__device__ __forceinline__ TileAt query_tile_at(const WattnParams& p, int nb, int v) {
+  TileAt t;
+  const int off = p.T - p.Tq;
+  for (int behind = 0; behind < 2; ++behind)
+    for (t.b = 0; t.b < p.B; ++t.b) {
+      // without lengths: every sequence alike, none behind
+      const int some = p.lengths ? min(nb, (max(seq_len(p, t.b) - off, 0) + 127) >> 7) : nb;
+      if (!p.lengths) {
+        t.b = v / (nb * p.H);
+        v %= nb * p.H;
+      }
+      const int tiles = behind ? nb - some : some, n = tiles * p.H;
+      if (v < n) {
+        t.h = p.heads_first ? v % p.H : v / tiles;
+        t.m = (behind ? nb : some) - 1 - (p.heads_first ? v / p.H : v % tiles);
+        return t;
+      }
+      v -= n;
+    }
+  t.b = t.h = t.m = 0;   // not reached: v is below B * H * nb
+  return t;
 }
 
 // Gradients of keys [kt BN, (kt + 1) BN): the queries that see any of them

@@ -149,11 +149,11 @@ struct QueryTile {
   int b, h, hk, q0, i0, len, sink_tiles, first, count;
   int narrow;   // the sink tile of which at most 32 keys are sinks, or -1
   __device__ __forceinline__ QueryTile(const WattnParams& p, int nb, int tile) {
-    const int bh = tile / nb;
-    b = bh / p.H;
-    h = bh % p.H;
+    const TileAt at = query_tile_at(p, nb, tile);
+    b = at.b;
+    h = at.h;
     hk = h / p.group;
-    q0 = (tile % nb) * 128;
+    q0 = at.m * 128;
     i0 = q0 + p.T - p.Tq;
     len = seq_len(p, b);
     const int last = min(min(i0 + 128, p.T), len) - 1;    // last position of the tile that is a token

@@ -159,13 +159,15 @@ static RotaryParams rotary_params(const lact_rotary_problem* p, const RotaryDims
 }
 
 // ------------------------------------------------------------------ window attention
-constexpr int kWattnFarRows = 1024;   // query rows of a sink tile's far part
+// Query rows of a sink tile's far part: about the work of a near part; the
+// CUDA cores take as long for a quarter of the rows.
+constexpr int kWattnFarRows = 1024, kWattnFarRowsF32 = 256;
 constexpr int kFewRounds = 8;         // rounds of persistent CTAs below which the short tiles go last
 
 struct WattnDims {
   int64_t B, H, Hkv, T, Tq, d, DP;
   int window, sinks, dtype;
-  int bn, sink_tiles, parts, key_tiles;   // of the keys' gradients
+  int bn, sink_tiles, parts, key_tiles, far_rows;   // of the keys' gradients
 };
 
 static int wattn_validate(const lact_swa_sink_problem* p, WattnDims& D) {
@@ -180,10 +182,11 @@ static int wattn_validate(const lact_swa_sink_problem* p, WattnDims& D) {
   D.window = static_cast<int>(std::min(p->window, p->T));
   D.sinks = static_cast<int>(std::min(p->sinks, p->T));
   D.dtype = p->dtype;
-  D.bn = D.dtype == LACT_F32 ? kSimtM : 128;
+  D.bn = D.dtype == LACT_BF16 ? 128 : D.DP <= 128 ? SimtCfg<128>::kM : SimtCfg<256>::kM;
+  D.far_rows = D.dtype == LACT_BF16 ? kWattnFarRows : kWattnFarRowsF32;
   D.key_tiles = static_cast<int>(cdiv(D.T, D.bn));
   D.sink_tiles = static_cast<int>(cdiv(D.sinks, D.bn));
-  const int far = far_parts(D.bn, D.window, static_cast<int>(D.T), kWattnFarRows);
+  const int far = far_parts(D.bn, D.window, static_cast<int>(D.T), D.far_rows);
   if (far == 0) D.sink_tiles = 0;   // the window reaches every query: no far part
   D.parts = 1 + far;
   return LACT_OK;
@@ -209,7 +212,7 @@ static WattnParams wattn_params(const WattnDims& D, float scale, const int32_t* 
   a.lse = const_cast<float*>(lse); a.lengths = lengths; a.scale = scale;
   a.B = static_cast<int>(D.B); a.H = static_cast<int>(D.H); a.Hkv = static_cast<int>(D.Hkv);
   a.group = static_cast<int>(D.H / D.Hkv); a.T = static_cast<int>(D.T); a.Tq = static_cast<int>(D.Tq);
-  a.d = static_cast<int>(D.d); a.window = D.window; a.sinks = D.sinks; a.far_rows = kWattnFarRows;
+  a.d = static_cast<int>(D.d); a.window = D.window; a.sinks = D.sinks; a.far_rows = D.far_rows;
   return a;
 }
 
@@ -259,8 +262,8 @@ static cudaError_t wattn_fwd_f32(const WattnDims& D, const WattnParams& a, cudaS
   static bool done[64] = {};
   const cudaError_t e = set_smem(k_wattn_fwd_f32<DP>, SimtCfg<DP>::kFwdSmem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(cdiv(D.Tq, kSimtM)), static_cast<unsigned>(D.B * D.H));
-  return launch_pdl(k_wattn_fwd_f32<DP>, grid, dim3(kSimtThreads), SimtCfg<DP>::kFwdSmem, st, a);
+  const dim3 grid(static_cast<unsigned>(cdiv(D.Tq, SimtCfg<DP>::kM)), static_cast<unsigned>(D.B * D.H));
+  return launch_pdl(k_wattn_fwd_f32<DP>, grid, dim3(SimtCfg<DP>::kThreads), SimtCfg<DP>::kFwdSmem, st, a);
 }
 template <int DP>
 static cudaError_t wattn_dq_f32(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
@@ -268,8 +271,8 @@ static cudaError_t wattn_dq_f32(const WattnDims& D, const WattnParams& a, cudaSt
   static_assert(SimtCfg<DP>::kBwdSmem <= kMaxSmemPerBlock, "dynamic shared memory above the per-CTA limit");
   const cudaError_t e = set_smem(k_wattn_dq_f32<DP>, SimtCfg<DP>::kBwdSmem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(cdiv(D.Tq, kSimtM)), static_cast<unsigned>(D.B * D.H));
-  return launch_pdl(k_wattn_dq_f32<DP>, grid, dim3(kSimtThreads), SimtCfg<DP>::kBwdSmem, st, a);
+  const dim3 grid(static_cast<unsigned>(cdiv(D.Tq, SimtCfg<DP>::kM)), static_cast<unsigned>(D.B * D.H));
+  return launch_pdl(k_wattn_dq_f32<DP>, grid, dim3(SimtCfg<DP>::kThreads), SimtCfg<DP>::kBwdSmem, st, a);
 }
 template <int DP>
 static cudaError_t wattn_dkv_f32(const WattnDims& D, const WattnParams& a, cudaStream_t st) {
@@ -278,7 +281,7 @@ static cudaError_t wattn_dkv_f32(const WattnDims& D, const WattnParams& a, cudaS
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(D.sink_tiles * D.parts + D.key_tiles - D.sink_tiles),
                   static_cast<unsigned>(D.B * D.Hkv));
-  return launch_pdl(k_wattn_dkv_f32<DP>, grid, dim3(kSimtThreads), SimtCfg<DP>::kBwdSmem, st, a, D.sink_tiles, D.parts);
+  return launch_pdl(k_wattn_dkv_f32<DP>, grid, dim3(SimtCfg<DP>::kThreads), SimtCfg<DP>::kBwdSmem, st, a, D.sink_tiles, D.parts);
 }
 
 template <int DP, int MODE>

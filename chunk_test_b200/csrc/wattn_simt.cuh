@@ -2,8 +2,9 @@
 // cores: float32 inputs, products and sums (the tensor cores would round the
 // operands).  Formulas and mask: wattn_common.cuh.
 //
-// Tiles of 64 rows against tiles of 32 in shared memory, 256 threads; a thread
-// holds 4 x 2 scores and 4 rows x (D/16) columns of each product that runs
+// Tiles of 32 rows (64 above d = 128) against tiles of 32 in shared memory, 4
+// threads a row; small tiles, so that a short sequence fills more SMs, as long as
+// two CTAs or more share one.  A thread holds 4 x 2 scores and 4 rows x (D/16) columns of each product that runs
 // over the other axis.  Bound by the FP32 pipe and the shared-memory reads
 // that feed it.
 #pragma once
@@ -12,12 +13,13 @@
 
 namespace lact {
 
-constexpr int kSimtM = 64, kSimtN = 32, kSimtThreads = 256;
+constexpr int kSimtN = 32;
 
 template <int D>
 struct SimtCfg {
+  static constexpr int kM = D <= 128 ? 32 : 64, kThreads = 4 * kM;
   static constexpr int kLd = D + 4;                     // row pitch: a row starts 4 banks after the last
-  static constexpr int kMain = kSimtM * kLd, kOther = kSimtN * kLd, kP = kSimtM * (kSimtN + 1);
+  static constexpr int kMain = kM * kLd, kOther = kSimtN * kLd, kP = kM * (kSimtN + 1);
   static constexpr int kFwdSmem = (kMain + 2 * kOther + kP) * 4;
   static constexpr int kBwdSmem = (2 * kMain + 2 * kOther + 2 * kP) * 4;
   static constexpr int kC = D / 16;                     // columns of a thread
@@ -28,7 +30,7 @@ struct SimtCfg {
 template <int ROWS, int D>
 __device__ __forceinline__ void simt_load(float* dst, const float* src, int64_t st, int r0, int begin, int end, int d) {
   constexpr int kV = D / 4;
-  for (int e = threadIdx.x; e < ROWS * kV; e += kSimtThreads) {
+  for (int e = threadIdx.x; e < ROWS * kV; e += SimtCfg<D>::kThreads) {
     const int r = e / kV, c = (e % kV) * 4, row = r0 + r;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row >= begin && row < end && c < d) v = *reinterpret_cast<const float4*>(src + row * st + c);
@@ -97,20 +99,20 @@ __device__ __forceinline__ bool wattn_sees(int i, int j, int window, int sinks, 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSimtThreads) k_wattn_fwd_f32(const WattnParams p) {
+__global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_fwd_f32(const WattnParams p) {
   using C = SimtCfg<D>;
   extern __shared__ float sm[];
   float *sq = sm, *sk = sq + C::kMain, *sv = sk + C::kOther, *sp = sv + C::kOther;
   griddep_launch();
   griddep_wait();
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H, hk = h / p.group;
-  const int q0 = blockIdx.x * kSimtM, off = p.T - p.Tq;
-  const int i0 = q0 + off, i1 = min(q0 + kSimtM, p.Tq) + off;
+  const int q0 = blockIdx.x * C::kM, off = p.T - p.Tq;
+  const int i0 = q0 + off, i1 = min(q0 + C::kM, p.Tq) + off;
   const int len = seq_len(p, b), tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const float* q = static_cast<const float*>(p.q.p) + b * p.q.sb + h * p.q.sh;
   const float* k = static_cast<const float*>(p.k.p) + b * p.k.sb + hk * p.k.sh;
   const float* v = static_cast<const float*>(p.v.p) + b * p.v.sb + hk * p.v.sh;
-  simt_load<kSimtM, D>(sq, q, p.q.st, q0, 0, min(p.Tq, len - off), p.d);
+  simt_load<C::kM, D>(sq, q, p.q.st, q0, 0, min(p.Tq, len - off), p.d);
   float acc[4][C::kC], m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -208,25 +210,25 @@ __global__ void __launch_bounds__(256) k_wattn_delta(const WattnParams p) {
   }
 }
 
-// dQ of 64 queries: over the key tiles, P = exp(S - lse), dS = P (dO V^T - delta) scale, dQ += dS K.
+// dQ of kM queries: over the key tiles, P = exp(S - lse), dS = P (dO V^T - delta) scale, dQ += dS K.
 template <int D>
-__global__ void __launch_bounds__(kSimtThreads) k_wattn_dq_f32(const WattnParams p) {
+__global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_dq_f32(const WattnParams p) {
   using C = SimtCfg<D>;
   extern __shared__ float sm[];
   float *sq = sm, *sg = sq + C::kMain, *sk = sg + C::kMain, *sv = sk + C::kOther, *sp = sv + C::kOther;
   griddep_launch();
   griddep_wait();
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H, hk = h / p.group;
-  const int q0 = blockIdx.x * kSimtM, off = p.T - p.Tq;
-  const int i0 = q0 + off, i1 = min(q0 + kSimtM, p.Tq) + off;
+  const int q0 = blockIdx.x * C::kM, off = p.T - p.Tq;
+  const int i0 = q0 + off, i1 = min(q0 + C::kM, p.Tq) + off;
   const int len = seq_len(p, b), tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const float* q = static_cast<const float*>(p.q.p) + b * p.q.sb + h * p.q.sh;
   const float* g = static_cast<const float*>(p.dout.p) + b * p.dout.sb + h * p.dout.sh;
   const float* k = static_cast<const float*>(p.k.p) + b * p.k.sb + hk * p.k.sh;
   const float* v = static_cast<const float*>(p.v.p) + b * p.v.sb + hk * p.v.sh;
   const int qend = min(p.Tq, len - off);
-  simt_load<kSimtM, D>(sq, q, p.q.st, q0, 0, qend, p.d);
-  simt_load<kSimtM, D>(sg, g, p.dout.st, q0, 0, qend, p.d);
+  simt_load<C::kM, D>(sq, q, p.q.st, q0, 0, qend, p.d);
+  simt_load<C::kM, D>(sg, g, p.dout.st, q0, 0, qend, p.d);
   float acc[4][C::kC] = {}, lse[4], del[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -271,11 +273,11 @@ __global__ void __launch_bounds__(kSimtThreads) k_wattn_dq_f32(const WattnParams
   }
 }
 
-// dK, dV of 64 keys over one part of the query positions (KeyPart) and the
+// dK, dV of kM keys over one part of the query positions (KeyPart) and the
 // group's heads: dV += P^T dO, dK += dS^T Q.  A sink tile's parts go to
-// `part` [B Hkv][sink tiles][parts][2][64][D], the others to dk and dv.
+// `part` [B Hkv][sink tiles][parts][2][kM][D], the others to dk and dv.
 template <int D>
-__global__ void __launch_bounds__(kSimtThreads) k_wattn_dkv_f32(const WattnParams p, int sink_tiles, int parts) {
+__global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_dkv_f32(const WattnParams p, int sink_tiles, int parts) {
   using C = SimtCfg<D>;
   extern __shared__ float sm[];
   float *sk = sm, *sv = sk + C::kMain, *sq = sv + C::kMain, *sg = sq + C::kOther, *sp = sg + C::kOther, *sd = sp + C::kP;
@@ -286,14 +288,14 @@ __global__ void __launch_bounds__(kSimtThreads) k_wattn_dkv_f32(const WattnParam
   const int kt = item < split ? item / parts : item - split + sink_tiles;
   const int part = item < split ? item % parts : 0;
   const int bk = blockIdx.y, b = bk / p.Hkv, hk = bk % p.Hkv;
-  const int j0 = kt * kSimtM, off = p.T - p.Tq, len = seq_len(p, b);
+  const int j0 = kt * C::kM, off = p.T - p.Tq, len = seq_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const KeyPart kp = key_part(kt, part, kSimtM, p.window, p.T, p.far_rows);
+  const KeyPart kp = key_part(kt, part, C::kM, p.window, p.T, p.far_rows);
   const int lo = max(kp.lo, off), hi = min(kp.hi, len);
   const float* k = static_cast<const float*>(p.k.p) + b * p.k.sb + hk * p.k.sh;
   const float* v = static_cast<const float*>(p.v.p) + b * p.v.sb + hk * p.v.sh;
-  simt_load<kSimtM, D>(sk, k, p.k.st, j0, 0, len, p.d);
-  simt_load<kSimtM, D>(sv, v, p.v.st, j0, 0, len, p.d);
+  simt_load<C::kM, D>(sk, k, p.k.st, j0, 0, len, p.d);
+  simt_load<C::kM, D>(sv, v, p.v.st, j0, 0, len, p.d);
   float ak[4][C::kC] = {}, av[4][C::kC] = {};
   for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
     const float* q = static_cast<const float*>(p.q.p) + b * p.q.sb + h * p.q.sh;
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_wattn_dkv_f32(const WattnParam
   }
   const bool direct = kt >= sink_tiles;
   float* po = direct ? nullptr
-                     : p.part + ((static_cast<int64_t>(bk) * sink_tiles + kt) * parts + part) * 2 * kSimtM * D;
+                     : p.part + ((static_cast<int64_t>(bk) * sink_tiles + kt) * parts + part) * 2 * C::kM * D;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = j0 + 4 * ty + i;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_wattn_dkv_f32(const WattnParam
       const float4 y = make_float4(av[i][4 * k4], av[i][4 * k4 + 1], av[i][4 * k4 + 2], av[i][4 * k4 + 3]);
       if (!direct) {
         *reinterpret_cast<float4*>(po + (4 * ty + i) * D + c) = x;
-        *reinterpret_cast<float4*>(po + (kSimtM + 4 * ty + i) * D + c) = y;
+        *reinterpret_cast<float4*>(po + (C::kM + 4 * ty + i) * D + c) = y;
       } else if (row < p.T && c < p.d) {
         *reinterpret_cast<float4*>(static_cast<float*>(p.dk.p) + b * p.dk.sb + hk * p.dk.sh + row * p.dk.st + c) = x;
         *reinterpret_cast<float4*>(static_cast<float*>(p.dv.p) + b * p.dv.sb + hk * p.dv.sh + row * p.dv.st + c) = y;

@@ -81,7 +81,7 @@ _P = ctypes.POINTER(LactProblem)
 _vp = ctypes.c_void_p
 _RP = ctypes.POINTER(LactRotaryProblem)
 _SP = ctypes.POINTER(LactSwaSinkProblem)
-_T4 = ctypes.POINTER(LactTensor4)
+_T4 = _vp   # lact_tensor4*: LactTensor4, or four int64 of an array
 # name -> (restype, argtypes); the exported surface of include/lact.h
 SIGNATURES = {
     "lact_ttt_workspace_bytes": (ctypes.c_size_t, [_P]),

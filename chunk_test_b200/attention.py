@@ -21,15 +21,27 @@ from ._abi import LactError
 _DT = {torch.float32: _abi.LACT_F32, torch.bfloat16: _abi.LACT_BF16}
 
 
-_T4, _byref = _abi.LactTensor4, ctypes.byref
+_byref = ctypes.byref
+_ARRAYS = tuple(ctypes.c_int64 * (4 * n) for n in range(9))
 
 
-def _ref(t):
-    """The tensor as a lact_tensor4 argument, or NULL."""
-    if t is None:
-        return None
-    s = t.stride()
-    return _byref(_T4(t.data_ptr(), s[0], s[1], s[2]))
+def _views(*tensors):
+    """The tensors as lact_tensor4 arguments (None: NULL), slices of one array."""
+    v, at = [], []
+    for t in tensors:
+        if t is None:
+            at.append(None)
+        else:
+            at.append(8 * len(v))
+            v.append(t.data_ptr())
+            v += t.stride()[:3]
+    a = _ARRAYS[len(v) // 4](*v)
+    return [None if x is None else _byref(a, x) for x in at]
+
+
+def _new(t):
+    """A new contiguous tensor like `t`."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _at(t):
@@ -163,15 +175,14 @@ def rotary_fwd(q, k, freqs, *, positions=None, start=0, interleaved=False, ampli
     p = _rotary_args(q, k, freqs, positions, start, interleaved, amplitude)
     _params(("q_scale", "q_offset", "k_scale", "k_offset"), (q_scale, q_offset, k_scale, k_offset), q, k)
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(k.shape, dtype=q.dtype, device=q.device))
+        out = (_new(q), None if k is None else _new(k))
     else:
         _tensor("out[0]", out[0], q.shape, q)
         if k is not None:
             _tensor("out[1]", out[1], k.shape, q)
-    _call("lact_rotary_fwd", q.device, stream, _byref(p), _ref(q), _ref(k), _at(freqs), _at(positions),
-          _at(q_scale), _at(q_offset), _at(k_scale), _at(k_offset), _ref(out[0]), _ref(None if k is None else
-          out[1]))
+    q_, k_, qo, ko = _views(q, k, out[0], None if k is None else out[1])
+    _call("lact_rotary_fwd", q.device, stream, _byref(p), q_, k_, _at(freqs), _at(positions), _at(q_scale),
+          _at(q_offset), _at(k_scale), _at(k_offset), qo, ko)
     return out[0], (None if k is None else out[1])
 
 
@@ -187,9 +198,9 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
     affine = _params(("q_scale", "k_scale"), (q_scale, k_scale), dq_out, dk_out)
     res = dict.fromkeys(("dq", "dk", "dq_scale", "dq_offset", "dk_scale", "dk_offset"))
     if out is None:
-        res["dq"] = torch.empty(dq_out.shape, dtype=dq_out.dtype, device=dq_out.device)
+        res["dq"] = _new(dq_out)
         if dk_out is not None:
-            res["dk"] = torch.empty(dk_out.shape, dtype=dq_out.dtype, device=dq_out.device)
+            res["dk"] = _new(dk_out)
     else:
         res["dq"] = _tensor("out[0]", out[0], dq_out.shape, dq_out)
         if dk_out is not None:
@@ -207,11 +218,11 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
         if need == 0:
             raise LactError(_abi.LACT_EINVAL, "lact_rotary_bwd_workspace_bytes")
         workspace = _workspace(workspace, need, dq_out.device)
-    _call("lact_rotary_bwd", dq_out.device, stream, _byref(p), _ref(dq_out), _ref(dk_out), _at(freqs),
-          _at(positions), _ref(q) if affine else None, _ref(k) if affine and dk_out is not None else None,
-          _at(q_scale), _at(k_scale), _ref(res["dq"]), _ref(res["dk"]), _at(res["dq_scale"]),
-          _at(res["dq_offset"]), _at(res["dk_scale"]), _at(res["dk_offset"]), _at(workspace) if affine else
-          None, need)
+    gq, gk, q_, k_, dq, dk = _views(dq_out, dk_out, q if affine else None,
+                                    k if affine and dk_out is not None else None, res["dq"], res["dk"])
+    _call("lact_rotary_bwd", dq_out.device, stream, _byref(p), gq, gk, _at(freqs), _at(positions), q_, k_,
+          _at(q_scale), _at(k_scale), dq, dk, _at(res["dq_scale"]), _at(res["dq_offset"]), _at(res["dk_scale"]),
+          _at(res["dk_offset"]), _at(workspace) if affine else None, need)
     return res
 
 
@@ -251,15 +262,15 @@ def swa_sink_fwd(q, k, v, window, sinks=0, *, lengths=None, scale=None, out=None
     p = _swa_sink_problem(q, k, window, sinks, scale, k.shape[2], q.shape[2])
     _keys(q, k, v, lengths)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _new(q)
     else:
         _tensor("out", out, q.shape, q)
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
     else:
         _dense("lse", lse, q.shape[:3], torch.float32, q.device)
-    _call("lact_swa_sink_fwd", q.device, stream, _byref(p), _ref(q), _ref(k), _ref(v), _at(lengths),
-          _ref(out), _at(lse))
+    q_, k_, v_, o_ = _views(q, k, v, out)
+    _call("lact_swa_sink_fwd", q.device, stream, _byref(p), q_, k_, v_, _at(lengths), o_, _at(lse))
     return out, lse
 
 
@@ -279,15 +290,16 @@ def swa_sink_bwd(q, k, v, out, lse, dout, window, sinks=0, *, lengths=None, scal
     _tensor("out", out, q.shape, q)
     _tensor("dout", dout, q.shape, q)
     _dense("lse", lse, q.shape[:3], torch.float32, q.device)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else _tensor("dq", dq, q.shape, q)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dk is None else _tensor("dk", dk, k.shape, q)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dv is None else _tensor("dv", dv, k.shape, q)
+    dq = _new(q) if dq is None else _tensor("dq", dq, q.shape, q)
+    dk = _new(k) if dk is None else _tensor("dk", dk, k.shape, q)
+    dv = _new(k) if dv is None else _tensor("dv", dv, k.shape, q)
     need = int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(_byref(p)))
     if need == 0:
         raise LactError(_abi.LACT_EINVAL, "lact_swa_sink_bwd_workspace_bytes")
     workspace = _workspace(workspace, need, q.device)
-    _call("lact_swa_sink_bwd", q.device, stream, _byref(p), _ref(q), _ref(k), _ref(v), _ref(out), _at(lse),
-          _ref(dout), _at(lengths), _ref(dq), _ref(dk), _ref(dv), _at(workspace), workspace.numel())
+    q_, k_, v_, o_, g_, dq_, dk_, dv_ = _views(q, k, v, out, dout, dq, dk, dv)
+    _call("lact_swa_sink_bwd", q.device, stream, _byref(p), q_, k_, v_, o_, _at(lse), g_, _at(lengths), dq_, dk_, dv_,
+          _at(workspace), workspace.numel())
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -315,11 +327,11 @@ def swa_sink_decode(q, k, v, k_cache, v_cache, seen, window, sinks=0, *, scale=N
     _caches(q, k, k_cache, v_cache, window, sinks)
     _dense("seen", seen, (B,), torch.int32, q.device)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _new(q)
     else:
         _tensor("out", out, q.shape, q)
-    _call("lact_swa_sink_decode", q.device, stream, _byref(p), _ref(q), _ref(k), _ref(v), _at(k_cache),
-          _at(v_cache), _at(seen), _ref(out))
+    q_, k_, v_, o_ = _views(q, k, v, out)
+    _call("lact_swa_sink_decode", q.device, stream, _byref(p), q_, k_, v_, _at(k_cache), _at(v_cache), _at(seen), o_)
     return out
 
 
@@ -332,5 +344,5 @@ def swa_cache_fill(k, v, k_cache, v_cache, window, sinks=0, *, lengths=None, str
     p = _swa_sink_problem(k, k, window, sinks, 1.0, T, 1)
     _keys(k, k, v, lengths)
     _caches(k, k, k_cache, v_cache, window, sinks)
-    _call("lact_swa_cache_fill", k.device, stream, _byref(p), _ref(k), _ref(v), _at(lengths), _at(k_cache),
-          _at(v_cache))
+    k_, v_ = _views(k, v)
+    _call("lact_swa_cache_fill", k.device, stream, _byref(p), k_, v_, _at(lengths), _at(k_cache), _at(v_cache))

@@ -71,6 +71,13 @@ static bool apart_from(const View4& a, const Extent4& e, int esz, const void* p,
   return !p || !overlaps(a.p, static_cast<size_t>(span(a, e)) * esz, p, static_cast<size_t>(bytes));
 }
 
+// A failed call's error is reported by its status alone, not left behind for the
+// caller's next check.
+static cudaError_t cleared(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
 // Raises a kernel's dynamic shared memory limit, once per device.
 template <class F>
 static cudaError_t set_smem(F* kernel, int bytes, bool (&done)[64], bool big_cluster = false) {
@@ -314,10 +321,10 @@ static cudaError_t wattn_bwd_bf16(const WattnDims& D, const WattnParams& a, cuda
 
 #define LACT_BY_DP(DPV, ...)                  \
   switch (DPV) {                               \
-    case 64: { constexpr int DP = 64; return __VA_ARGS__; }   \
-    case 128: { constexpr int DP = 128; return __VA_ARGS__; } \
-    case 192: { constexpr int DP = 192; return __VA_ARGS__; } \
-    default: { constexpr int DP = 256; return __VA_ARGS__; }  \
+    case 64: { constexpr int DP = 64; return cleared(__VA_ARGS__); }   \
+    case 128: { constexpr int DP = 128; return cleared(__VA_ARGS__); } \
+    case 192: { constexpr int DP = 192; return cleared(__VA_ARGS__); } \
+    default: { constexpr int DP = 256; return cleared(__VA_ARGS__); }  \
   }
 
 template <typename T, int LANES>
@@ -349,7 +356,7 @@ static void wattn_fwd_run(const WattnDims& D, const WattnParams& a, cudaStream_t
 
 static void wattn_bwd_run(const WattnDims& D, const WattnParams& a, cudaStream_t st, Launcher& L) {
   L.st = st;
-  L(K_WATTN_ELEM, [&] { return launch_wattn_delta(D, a, st); });
+  L(K_WATTN_ELEM, [&] { return cleared(launch_wattn_delta(D, a, st)); });
   L(K_WATTN_DQ, [&]() -> cudaError_t {
     LACT_BY_DP(D.DP, D.dtype == LACT_F32 ? wattn_dq_f32<DP>(D, a, st) : (wattn_bwd_bf16<DP, WATTN_DQ>(D, a, st)))
   });
@@ -358,13 +365,13 @@ static void wattn_bwd_run(const WattnDims& D, const WattnParams& a, cudaStream_t
   } else {
     // both in one pass where TMEM holds both accumulators beside S and dP
     if (D.DP <= 128) {
-      L(K_WATTN_DKV, [&] { return D.DP == 64 ? wattn_bwd_bf16<64, WATTN_DKV>(D, a, st) : wattn_bwd_bf16<128, WATTN_DKV>(D, a, st); });
+      L(K_WATTN_DKV, [&] { return cleared(D.DP == 64 ? wattn_bwd_bf16<64, WATTN_DKV>(D, a, st) : wattn_bwd_bf16<128, WATTN_DKV>(D, a, st)); });
     } else {
-      L(K_WATTN_DKV, [&] { return D.DP == 192 ? wattn_bwd_bf16<192, WATTN_DK>(D, a, st) : wattn_bwd_bf16<256, WATTN_DK>(D, a, st); });
-      L(K_WATTN_DKV, [&] { return D.DP == 192 ? wattn_bwd_bf16<192, WATTN_DV>(D, a, st) : wattn_bwd_bf16<256, WATTN_DV>(D, a, st); });
+      L(K_WATTN_DKV, [&] { return cleared(D.DP == 192 ? wattn_bwd_bf16<192, WATTN_DK>(D, a, st) : wattn_bwd_bf16<256, WATTN_DK>(D, a, st)); });
+      L(K_WATTN_DKV, [&] { return cleared(D.DP == 192 ? wattn_bwd_bf16<192, WATTN_DV>(D, a, st) : wattn_bwd_bf16<256, WATTN_DV>(D, a, st)); });
     }
   }
-  if (D.sink_tiles > 0) L(K_WATTN_ELEM, [&] { return launch_wattn_sums(D, a, st); });
+  if (D.sink_tiles > 0) L(K_WATTN_ELEM, [&] { return cleared(launch_wattn_sums(D, a, st)); });
 }
 
 // ------------------------------------------------------------------ single-token form
@@ -466,7 +473,7 @@ int lact_rotary_fwd(const lact_rotary_problem* p, const lact_tensor4* q, const l
   a.q_scale = q_scale; a.q_offset = q_offset; a.k_scale = k_scale; a.k_offset = k_offset;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   Launcher L{false, st};
-  L(K_ROTARY, [&] { return affine ? launch_rotary_any<false, true>(p, r, a, st) : launch_rotary_any<false, false>(p, r, a, st); });
+  L(K_ROTARY, [&] { return cleared(affine ? launch_rotary_any<false, true>(p, r, a, st) : launch_rotary_any<false, false>(p, r, a, st)); });
   return L.err;
 }
 
@@ -519,13 +526,13 @@ int lact_rotary_bwd(const lact_rotary_problem* p, const lact_tensor4* dq_out, co
   a.q_scale = q_scale; a.k_scale = k_scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   Launcher L{false, st};
-  L(K_ROTARY, [&] { return affine ? launch_rotary_any<true, true>(p, r, a, st) : launch_rotary_any<true, false>(p, r, a, st); });
+  L(K_ROTARY, [&] { return cleared(affine ? launch_rotary_any<true, true>(p, r, a, st) : launch_rotary_any<true, false>(p, r, a, st)); });
   if (affine)
     L(K_ROTARY_SUMS, [&] {
       const int64_t n = 2 * (p->H + p->Hkv) * p->d;
-      return launch_pdl(k_rotary_sums, dim3(static_cast<unsigned>(cdiv(n, 32))), dim3(512), 0, st,
-                        static_cast<const float*>(a.partial), static_cast<int>(p->B * r.ranges), a.H, a.Hkv, a.d, dq_scale,
-                        dq_offset, dk_scale, dk_offset);
+      return cleared(launch_pdl(k_rotary_sums, dim3(static_cast<unsigned>(cdiv(n, 32))), dim3(512), 0, st,
+                                static_cast<const float*>(a.partial), static_cast<int>(p->B * r.ranges), a.H, a.Hkv,
+                                a.d, dq_scale, dq_offset, dk_scale, dk_offset));
     });
   return L.err;
 }
@@ -628,7 +635,7 @@ int lact_swa_sink_decode(const lact_swa_sink_problem* p, const lact_tensor4* q, 
   a.hgroups = static_cast<int>(cdiv(a.group, kDecHeads));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   Launcher L{false, st};
-  L(K_WATTN_DECODE, [&] { return launch_decode_any(rup(p->d, 64), p->dtype, a, p->B * p->Hkv * a.hgroups, st); });
+  L(K_WATTN_DECODE, [&] { return cleared(launch_decode_any(rup(p->d, 64), p->dtype, a, p->B * p->Hkv * a.hgroups, st)); });
   return L.err;
 }
 
@@ -657,7 +664,7 @@ int lact_swa_cache_fill(const lact_swa_sink_problem* p, const lact_tensor4* k, c
   Launcher L{false, st};
   L(K_WATTN_ELEM, [&] {
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(cdiv(a.n * a.row_vecs, 256), kPlanSMs * 16)));
-    return launch_pdl(k_wattn_fill, grid, dim3(256), 0, st, a);
+    return cleared(launch_pdl(k_wattn_fill, grid, dim3(256), 0, st, a));
   });
   return L.err;
 }

@@ -135,3 +135,51 @@ def test_on_another_stream():
     ct.swa_sink_decode(q, k, v, kc, vc, pos, 36, 4, out=out, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(out, want) and torch.equal(kc, k2) and torch.equal(vc, v2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_cache_past_32_bit_offsets(dtype):
+    """A cache of 2^31 elements and more: the last slots hold the keys that
+    matter, the others zeros with scores far below."""
+    d, sinks = 256, 4
+    window = 2 ** 31 // d + 300
+    C = sinks + window
+    kc = torch.zeros((1, 1, C, d), dtype=dtype, device="cuda")
+    vc = torch.zeros((1, 1, C, d), dtype=dtype, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, k, v = (torch.randn((1, 1, 1, d), generator=g, device="cuda").to(dtype) for _ in range(3))
+    # scores near 40 against 0 for the zero keys: exp(-40) * 2^23 of them leave 2^-34 of the weight
+    tail = torch.randn((16, d), generator=g, device="cuda")
+    qf = q[0, 0, 0].float()
+    tail += (40.0 * 16.0 - tail @ qf)[:, None] * qf / (qf @ qf)
+    kc[0, 0, -16:] = tail.to(dtype)
+    vc[0, 0, -16:] = torch.randn((16, d), generator=g, device="cuda").to(dtype)
+    k.copy_(kc[0, 0, -1])
+    pos = torch.tensor([C - 2], dtype=torch.int32, device="cuda")    # the new token takes the slot before the last
+    out = ct.swa_sink_decode(q, k, v, kc, vc, pos, window, sinks)
+    keys = torch.cat((kc[0, 0, -16:-2], k[0, 0])).double()
+    vals = torch.cat((vc[0, 0, -16:-2], v[0, 0])).double()
+    p = torch.softmax(keys @ q[0, 0, 0].double() / math.sqrt(d), 0)
+    assert torch.equal(kc[0, 0, -2], k[0, 0, 0]) and torch.equal(vc[0, 0, -2], v[0, 0, 0])
+    # the zero keys' weight is below 2^-30 of the sum; scores of 40 in 32 bits are off by 2^-18 of them at most
+    over = (out[0, 0, 0].double() - p @ vals).abs()
+    u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+    bound = u * (p @ vals).abs() + ((u if dtype == BF16 else 0) + 2.0 ** -12) * (p @ vals.abs())
+    assert float((over / bound).max()) <= 1.0, float((over / bound).max())
+
+
+def test_refused_on_the_gpu():
+    q, k, v, kc, vc = make(2, 2, 1, 40, 64, BF16)
+    pos = torch.tensor([3, 50], dtype=torch.int32, device="cuda")
+    want = ct.swa_sink_decode(q, k, v, kc, vc, pos, 36, 4)
+    with pytest.raises(ValueError):
+        ct.swa_sink_decode(q, k, v, kc, vc, pos, 37, 4)          # not the cache's size
+    with pytest.raises(ValueError):
+        ct.swa_sink_decode(q, k, v, kc[:, :, :39], vc, pos, 36, 4)
+    with pytest.raises(ValueError):
+        ct.swa_sink_decode(q.expand(2, 2, 3, 64), k, v, kc, vc, pos, 36, 4)
+    with pytest.raises(ValueError):
+        ct.swa_sink_decode(q, k, v, kc, vc, pos.long(), 36, 4)
+    with pytest.raises(ct.LactError):
+        ct.swa_sink_decode(q, k, v, kc, kc, pos, 36, 4)          # one buffer for both
+    assert torch.equal(ct.swa_sink_decode(q, k, v, kc, vc, pos, 36, 4), want)

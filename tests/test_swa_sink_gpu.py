@@ -189,3 +189,87 @@ def test_long_sequence_far_sinks():
     w = ao.attention(q, k, v, window, sinks, dout=dout)
     check_forward(out, lse, w, BF16, d, window + sinks)
     check_backward(ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks), w, BF16, d, T)
+
+
+def test_captured_and_replayed():
+    """A captured forward and backward, replayed on new values in the same
+    buffers, twice, while an uncaptured call of the same inputs runs before."""
+    q, k, v, dout = make(2, 4, 2, 400, 400, 128, BF16, "bthd")
+    lens = torch.tensor([400, 131], dtype=torch.int32, device="cuda")
+
+    def step():
+        out, lse = ct.swa_sink_fwd(q, k, v, 100, 4, lengths=lens)
+        return [out, lse] + list(ct.swa_sink_bwd(q, k, v, out, lse, dout, 100, 4, lengths=lens).values())
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (5, 6):
+        for x, y in zip((q, k, v, dout), make(2, 4, 2, 400, 400, 128, BF16, "bthd", seed=seed)):
+            x.copy_(y)
+        lens.copy_(torch.tensor([400 - seed, 200 + seed], dtype=torch.int32))
+        graph.replay()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    assert ct.status() == ct.LACT_OK
+
+
+def test_two_streams_at_once():
+    """Backward passes in flight on two streams, each with its own workspace, give what they give alone."""
+    cases = [make(1, 4, 2, 1500, 1500, d, BF16, seed=d) for d in (128, 256)]
+    fwd = [ct.swa_sink_fwd(q, k, v, 300, 4) for q, k, v, _ in cases]
+    alone = [ct.swa_sink_bwd(q, k, v, *f, g, 300, 4) for (q, k, v, g), f in zip(cases, fwd)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    res = [[], []]
+    for _ in range(3):
+        for i, ((q, k, v, g), f) in enumerate(zip(cases, fwd)):
+            with torch.cuda.stream(streams[i]):
+                res[i].append(ct.swa_sink_bwd(q, k, v, *f, g, 300, 4))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in res[i]:
+            for n in r:
+                assert torch.equal(r[n], alone[i][n]), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,H,Hkv,d", [(1, 16, 1, 64), (5, 3, 3, 40), (130, 2, 1, 16)])
+def test_many_heads_and_batches(B, H, Hkv, d, dtype):
+    T, window, sinks = 140, 33, 2
+    q, k, v, dout = make(B, H, Hkv, T, T, d, dtype)
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks)
+    w = ao.attention(q, k, v, window, sinks, dout=dout)
+    check_forward(out, lse, w, dtype, d, window + sinks)
+    check_backward(ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks), w, dtype, d, T * (H // Hkv))
+
+
+def test_refused_on_the_gpu():
+    q, k, v, dout = make(1, 2, 1, 64, 64, 64, BF16)
+    out, lse = ct.swa_sink_fwd(q, k, v, 8, 1)
+    with pytest.raises(ct.LactError):
+        ct.swa_sink_fwd(q, k, v, 0, 1)                           # no window
+    with pytest.raises(ct.LactError):
+        ct.swa_sink_fwd(q, k, v, 8, -1)
+    with pytest.raises(ct.LactError):
+        ct.swa_sink_fwd(q, k, v, 8, 1, scale=-1.0)
+    with pytest.raises(ct.LactError):
+        ct.swa_sink_fwd(q, k, v, 8, 1, out=q)                    # onto an input
+    with pytest.raises(ct.LactError):
+        ct.swa_sink_bwd(q, k, v, out, lse, dout[:, :1].expand(1, 2, 64, 64)[:, :, :1].expand_as(q), 8, 1)  # stride 0
+    with pytest.raises(ValueError):
+        ct.swa_sink_fwd(q, k.float(), v, 8, 1)
+    with pytest.raises(ValueError):
+        ct.swa_sink_fwd(q, k, v[:, :, :-1], 8, 1)
+    with pytest.raises(ValueError):
+        ct.swa_sink_fwd(q.transpose(2, 3).contiguous().transpose(2, 3), k, v, 8, 1)   # channels apart
+    with pytest.raises(ValueError):
+        ct.swa_sink_fwd(q, k, v, 8, 1, lengths=torch.tensor([64], device="cuda"))     # int64
+    with pytest.raises(ValueError):
+        ct.swa_sink_bwd(q, k, v, out, lse, dout, 8, 1, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(TypeError):
+        ct.swa_sink_fwd(q.half(), k.half(), v.half(), 8, 1)
+    assert torch.equal(ct.swa_sink_fwd(q, k, v, 8, 1)[0], out)   # and the next call is as good as the first

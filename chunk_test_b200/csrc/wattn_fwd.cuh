@@ -25,8 +25,6 @@
 // (2048 clocks a tile at d = 256) above.
 #pragma once
 
-#include <type_traits>
-
 #include "swa_flash.cuh"
 #include "wattn_common.cuh"
 
@@ -133,6 +131,12 @@ __device__ __forceinline__ uint32_t visible_bits(int lo, int hi, int sk, int bas
 
 // Shared-memory descriptors of one operand differ by their start address only.
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+// Keeps the compiler from forming a loop's descriptors ahead of the loop, where
+// they spill.
+__device__ __forceinline__ uint64_t here(uint64_t desc) {
+  asm volatile("" : "+l"(desc));
+  return desc;
+}
 
 struct WattnFwdParams {
   CUtensorMap tmQ;          // [d, Tq, H, B], box {64, 128}
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
 
-  if (warp == 0 || warp == 6) {
+  if (warp == 0 || (NS == 2 && warp == 6)) {
     // ---------------------------------------------------------- producers
     if (lane == 0) {
       const bool keys = warp == 0, values = NS == 1 || warp == 6;
@@ -298,12 +302,12 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
           const int s = ik % KR;
           if (!mbar_wait(&kfull[s], (ik / KR) & 1)) return false;
           tc_fence_after();
+          const uint64_t qk = here(desc_at(qd, ks * C::kKBlk * 16384)), kk = here(desc_at(kd, s * C::kKSlot));
 #pragma unroll
           for (int kb = 0; kb < C::kKBlk; ++kb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_bf16(sd, desc_at(qd, (ks * C::kKBlk + kb) * 16384 + k * 32),
-                        desc_at(kd, s * C::kKSlot + kb * 16384 + k * 32), id, (ks | kb | k) ? 1u : 0u);
+              umma_bf16(sd, desc_at(qk, kb * 16384 + k * 32), desc_at(kk, kb * 16384 + k * 32), id, (ks | kb | k) ? 1u : 0u);
           umma_commit(&kempty[s]);
         }
         umma_commit(&sfull[sc % NS]);
@@ -316,10 +320,12 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
           const int s = iv % VR;
           if (!mbar_wait(&vfull[s], (iv / VR) & 1)) return false;
           tc_fence_after();
+          const uint64_t vk = here(desc_at(vd, s * C::kVSlot));
 #pragma unroll
           for (int k = 0; k < C::kVKeys / 16; ++k)
             if (k < 2 || !narrow)
-              umma_bf16_ta(tmem + C::kColO, pa + (vs * C::kVKeys + k * 16) / 2, desc_at(vd, s * C::kVSlot + k * 2048),
+              umma_bf16_ta(tmem + C::kColO, pa + vs * C::kVKeys / 2 + k * 8,
+                           desc_at(vk, k * 2048),
                            ido, (first && vs == 0 && k == 0) ? 0u : 1u);
           umma_commit(&vempty[s]);
         }
@@ -359,18 +365,24 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
     int sc = 0, iv = 0, tc = 0, nst = 0;
     bool ok = true;
     float mx, sum;
-    // one key tile of N columns; false where a wait gave up
-    auto step = [&](const QueryTile& t, int n, auto cols) -> bool {
-      constexpr int N = decltype(cols)::value;
+    // one key tile; false where a wait gave up
+    auto step = [&](const QueryTile& t, int n) -> bool {
+      const bool narrow = n == t.narrow;
+      const int cols = narrow ? 32 : 128;
       const int sb = sc % NS, j0 = t.key0(n), i = t.i0 + r, last = t.i0 + 127;
       if (!mbar_wait_warp(&sfull[sb], (sc / NS) & 1)) return false;
       tc_fence_after();
       const uint32_t ts = tq + C::kColS + sb * 128;
-      const bool whole = j0 + N - 1 <= t.i0 && (j0 > last - window || j0 + N - 1 < sinks) && last < t.len;
+      const bool whole = !narrow && j0 + 127 <= t.i0 && (j0 > last - window || j0 + 127 < sinks) && last < t.len;
       const int hi = i < t.len ? i - j0 : -1, lo = i - window - j0, sk = sinks - j0;
-      // scores of columns [c0, c0 + W), the others' at -inf
-      auto load = [&](float* sv, int c0, auto width) {
-        constexpr int W = decltype(width)::value;
+      // W columns at a time, as far as the tile goes (a narrow one: the first W, masked
+      // behind its 32).  The upper half is loaded twice, for the maximum and for the
+      // exponentials: a row of 128 scores in registers spills where two CTAs share an
+      // SM.  Two threads a row, which meet for the maximum, measured 137 us on the
+      // ragged batch where this takes 107.
+      constexpr int W = 64;
+      // scores of columns [c0, c0 + W), at -inf where they are not visible
+      auto load = [&](float* sv, int c0) {
 #pragma unroll
         for (int c = 0; c < W; c += 32) tmem_ld32(ts + c0 + c, sv + c);
         tmem_ld_wait();
@@ -384,14 +396,11 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
           }
         }
       };
-      // The upper half is loaded twice, for the maximum and for the exponentials:
-      // a row of 128 scores in registers spills where two CTAs share an SM.
-      constexpr int W = N < 64 ? N : 64;
-      using Width = std::integral_constant<int, W>;
       float sv[W], b4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c0 = N - W; c0 >= 0; c0 -= W) {
-        load(sv, c0, Width());
+      for (int c0 = 128 - W; c0 >= 0; c0 -= W) {
+        if (c0 >= cols) continue;
+        load(sv, c0);
 #pragma unroll
         for (int c = 0; c < W; c += 8) {
           b4[0] = max3(b4[0], sv[c], sv[c + 1]);
@@ -429,8 +438,9 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
       const float off = mx == -INFINITY ? 0.f : -mx * c2;
       float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c0 = 0; c0 < N; c0 += W) {
-        if (c0 > 0) load(sv, c0, Width());
+      for (int c0 = 0; c0 < 128; c0 += W) {
+        if (c0 >= cols) break;
+        if (c0 > 0) load(sv, c0);
 #pragma unroll
         for (int w = 0; w < W; w += 32) {
           uint32_t hw[16];
@@ -443,13 +453,13 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
             ps[c & 1] = add_f32x2(ps[c & 1], e);
             hw[c] = pack_bf16x2(e.x, e.y);   // the second product's operand: half a step, 2^-8 of each
           }
-          tmem_st16u(ts + (c0 + w) / 2, hw);
+          tmem_st16u(ts + (c0 + w) / 2, hw);   // over columns that this thread has read
         }
       }
       sum += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
       // value rows behind the sequence: a probability of 0 times whatever is there must stay 0
-      constexpr int per = N == 128 ? C::kVPer : 1, rows = N == 128 ? C::kVKeys : N;
-      if (t.len < j0 + N) {
+      const int per = narrow ? 1 : C::kVPer, rows = narrow ? 32 : C::kVKeys;
+      if (t.len < j0 + cols) {
         for (int vs = 0; vs < per; ++vs) {
           const int s = (iv + vs) % VR, keep = max(t.len - (j0 + vs * rows), 0);
           if (!mbar_wait_warp(&vfull[s], ((iv + vs) / VR) & 1)) return false;
@@ -472,7 +482,7 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
       mx = -INFINITY;
       sum = 0.f;
       for (int n = 0; ok && n < t.count; ++n)
-        ok = n == t.narrow ? step(t, n, std::integral_constant<int, 32>()) : step(t, n, std::integral_constant<int, 128>());
+        ok = step(t, n);
       if (!ok) break;
       // out = O / sum, lse = the reference maximum + log sum
       const bool in = t.q0 + r < p.a.Tq;

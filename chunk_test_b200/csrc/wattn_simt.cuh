@@ -103,7 +103,6 @@ __global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_fwd_f32(const Wa
   using C = SimtCfg<D>;
   extern __shared__ float sm[];
   float *sq = sm, *sk = sq + C::kMain, *sv = sk + C::kOther, *sp = sv + C::kOther;
-  griddep_launch();
   griddep_wait();
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H, hk = h / p.group;
   const int q0 = blockIdx.x * C::kM, off = p.T - p.Tq;
@@ -161,6 +160,7 @@ __global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_fwd_f32(const Wa
     __syncwarp();   // a warp reads only the rows of P that it wrote
     simt_mul<D>(sp, sv, ty, tx, acc);
   }
+  griddep_launch();   // not before: the next kernel's blocks would pile up on the SMs that this one leaves free
   float* o = static_cast<float*>(p.out.p) + b * p.out.sb + h * p.out.sh;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -216,7 +216,6 @@ __global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_dq_f32(const Wat
   using C = SimtCfg<D>;
   extern __shared__ float sm[];
   float *sq = sm, *sg = sq + C::kMain, *sk = sg + C::kMain, *sv = sk + C::kOther, *sp = sv + C::kOther;
-  griddep_launch();
   griddep_wait();
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H, hk = h / p.group;
   const int q0 = blockIdx.x * C::kM, off = p.T - p.Tq;
@@ -258,6 +257,7 @@ __global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_dq_f32(const Wat
     __syncwarp();
     simt_mul<D>(sp, sk, ty, tx, acc);
   }
+  griddep_launch();
   float* o = static_cast<float*>(p.dq.p) + b * p.dq.sb + h * p.dq.sh;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -281,7 +281,6 @@ __global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_dkv_f32(const Wa
   using C = SimtCfg<D>;
   extern __shared__ float sm[];
   float *sk = sm, *sv = sk + C::kMain, *sq = sv + C::kMain, *sg = sq + C::kOther, *sp = sg + C::kOther, *sd = sp + C::kP;
-  griddep_launch();
   griddep_wait();
   // blockIdx.x: the sink tiles' parts first, then the other tiles
   const int item = blockIdx.x, split = sink_tiles * parts;
@@ -326,6 +325,7 @@ __global__ void __launch_bounds__(SimtCfg<D>::kThreads) k_wattn_dkv_f32(const Wa
       simt_mul<D>(sd, sq, ty, tx, ak);
     }
   }
+  griddep_launch();
   const bool direct = kt >= sink_tiles;
   float* po = direct ? nullptr
                      : p.part + ((static_cast<int64_t>(bk) * sink_tiles + kt) * parts + part) * 2 * C::kM * D;

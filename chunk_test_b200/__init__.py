@@ -3,7 +3,9 @@
 The layer runs entirely in liblact_b200.so (hand-written tcgen05/TMA kernels
 for the bf16 path, CUDA-core kernels for the fp32 path) behind the C ABI of
 include/lact.h.  This package is the thin Python binding: `ttt_fwd` takes
-torch CUDA tensors, `ttt_fwd_host` takes host tensors.
+torch CUDA tensors, `ttt_fwd_host` takes host tensors.  The block's attention
+half (rotary positions, window attention with sinks, its gradient and its
+single-token form) is in attention.py.
 """
 from ._abi import (  # noqa: F401
     APPLY_THEN_UPDATE, UPDATE_THEN_APPLY, RULE_GD, RULE_MOMENTUM, RULE_MUON,

@@ -5,15 +5,16 @@
 //   dQ = scale dS K        a CTA holds 128 queries and walks their key tiles
 //   dK = scale dS^T Q      a CTA holds 128 keys and walks the queries that see
 //   dV = P^T dout          them, over the group's heads
-// One kernel, three modes; each gradient is accumulated by one CTA in TMEM, so
-// there are no atomics and the order of every sum is fixed.  S (and dout V^T)
-// are formed again for each of the three: 8 products where 5 would do with
-// 512 + 256 columns of accumulators at d = 256, and TMEM has 512.
+// One kernel, four modes: dQ, dK and dV in one (d <= 128), dK, dV (above).  Each
+// gradient is accumulated by one CTA in TMEM, so there are no atomics and the
+// order of every sum is fixed.  S and dout V^T are formed again for each mode: 7
+// products up to d = 128 and 8 above, where 5 would do with all accumulators in
+// TMEM beside S and dP; it has 512 columns.
 //
 // Resident operands A1 (Q or K) and A2 (dout or V), 128 rows; streamed tiles
 // of 128 rows B1 (K or Q) and B2 (V or dout).  128, because a product of N = 64
 // takes as long as one of N = 128: both read the same 4 KB of A per 16 channels
-// (tiles of 64 rows measured 1589 us where this takes TIME_A at B 2, H 6, T 8192,
+// (tiles of 64 rows measured 1589 us where 128 took 1035 at B 2, H 6, T 8192,
 // d 256, window 2048).  Roles:
 //   warp 0      TMA producer of A and B1.
 //   warp 10     TMA producer of B2.
@@ -22,9 +23,13 @@
 //               dP(n+1), and S(n+1) where TMEM holds two (d <= 128, dV), while
 //               dS(n) is computed.
 //   warps 2-9   dS (dV: P): two threads per row, 64 columns each.
-// Bound by the elementwise work up to d = 128 (a tile has 16384 exponentials, 1024
-// clocks, and as many differences and products); at d = 256 by the chain S, dS, dX of
-// one tile, for TMEM holds one S beside 256 columns of dX, and shared memory one B1.
+// Bound by latency: up to d = 128 by the elementwise work of a tile (16384
+// exponentials, 1024 clocks, and as many differences and products), which the
+// passes of 9 tiles repeat; at d = 256 by the chain S, dS, dX of one tile (about
+// 5000 clocks for 3072 of products), for TMEM holds one S beside 256 columns of
+// dX, and shared memory one B1.  Measured: B 2, H 6, T 8192, d 256, window 2048,
+// 4 sinks: dQ 327 us, dK and dV 580; B 2, 12 heads on 4, T 4001, d 128, window
+// 1000, 8 sinks: 103 and 174.
 #pragma once
 
 #include "wattn_fwd.cuh"

@@ -20,9 +20,12 @@
 // CTA's products run under the other's exponentials.  Above: one CTA per SM
 // and two score buffers (NS = 2).
 //
-// Bound by the exponentials (16 per clock and SM: 1024 clocks a tile of 128 x
-// 128, as many as both products at d = 128) up to d = 128, by the tensor pipe
-// (2048 clocks a tile at d = 256) above.
+// Bound, above d = 128, by the tensor pipe and what the issuing thread waits:
+// about 3000 clocks a tile for 2048 of products at d = 256 (B 2, H 6, T 32768,
+// window 2048, 4 sinks: 718 us, 1115 TFLOP/s).  Up to d = 128 by the latency of
+// S, softmax and P V in turn: 2900 clocks a tile and SM for 1024 of products and
+// as many of exponentials at 16 per clock (B 3 of up to 5000 tokens, 12 heads on
+// 4, d 128, window 1000: 107 us).
 #pragma once
 
 #include "swa_flash.cuh"

@@ -79,9 +79,7 @@ class LactError(RuntimeError):
 
 _P = ctypes.POINTER(LactProblem)
 _vp = ctypes.c_void_p
-_RP = ctypes.POINTER(LactRotaryProblem)
-_SP = ctypes.POINTER(LactSwaSinkProblem)
-_T4 = _vp   # lact_tensor4*: LactTensor4, or four int64 of an array
+_RP = _SP = _T4 = _vp   # lact_rotary_problem*, lact_swa_sink_problem*, lact_tensor4*: a Structure, or its bytes
 # name -> (restype, argtypes); the exported surface of include/lact.h
 SIGNATURES = {
     "lact_ttt_workspace_bytes": (ctypes.c_size_t, [_P]),

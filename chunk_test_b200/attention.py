@@ -10,8 +10,8 @@ device, on torch's current stream there (or `stream=`).
 """
 from __future__ import annotations
 
-import ctypes
 import math
+import struct
 
 import torch
 
@@ -21,22 +21,19 @@ from ._abi import LactError
 _DT = {torch.float32: _abi.LACT_F32, torch.bfloat16: _abi.LACT_BF16}
 
 
-_byref = ctypes.byref
-_ARRAYS = tuple(ctypes.c_int64 * (4 * n) for n in range(9))
+# The C structs are packed into bytes, whose address ctypes passes: a quarter of
+# the time of a ctypes.Structure, and these calls count microseconds.
+_TENSOR = struct.Struct("=4q").pack          # lact_tensor4
+_ROTARY = struct.Struct("=7qiifi").pack      # lact_rotary_problem
+_SINK = struct.Struct("=8qfi").pack          # lact_swa_sink_problem
 
 
-def _views(*tensors):
-    """The tensors as lact_tensor4 arguments (None: NULL), slices of one array."""
-    v, at = [], []
-    for t in tensors:
-        if t is None:
-            at.append(None)
-        else:
-            at.append(8 * len(v))
-            v.append(t.data_ptr())
-            v += t.stride()[:3]
-    a = _ARRAYS[len(v) // 4](*v)
-    return [None if x is None else _byref(a, x) for x in at]
+def _view(t):
+    """The tensor as a lact_tensor4, or NULL."""
+    if t is None:
+        return None
+    s = t.stride()
+    return _TENSOR(t.data_ptr(), s[0], s[1], s[2])
 
 
 def _new(t):
@@ -50,17 +47,17 @@ def _at(t):
 
 def _tensor(name, t, shape, like):
     """A [B, heads, T, d] tensor of `like`'s dtype and device, channels contiguous."""
-    if t.dtype is not like.dtype or t.device != like.device:
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.stride(3) != 1 and shape[3] > 1:
+    if t.stride()[3] != 1 and shape[3] > 1:
         raise ValueError(f"{name}'s channels must be contiguous")
     return t
 
 
 def _dense(name, t, shape, dtype, device):
-    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != device.index or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
     return t
 
@@ -143,8 +140,8 @@ def _rotary_args(q, k, freqs, positions, start, interleaved, amplitude):
     _dense("freqs", freqs, (freqs.shape[0],), torch.float64, q.device)
     if positions is not None:
         _dense("positions", positions, (B, T), torch.int32, q.device)
-    return _abi.LactRotaryProblem(B, H, Hkv, T, d, 2 * freqs.shape[0], int(start), int(bool(interleaved)),
-                                  _DT[q.dtype], float(amplitude), 0)
+    return _ROTARY(B, H, Hkv, T, d, 2 * freqs.shape[0], int(start), int(bool(interleaved)), _DT[q.dtype],
+                   float(amplitude), 0)
 
 
 def _params(names, values, q, k):
@@ -180,9 +177,8 @@ def rotary_fwd(q, k, freqs, *, positions=None, start=0, interleaved=False, ampli
         _tensor("out[0]", out[0], q.shape, q)
         if k is not None:
             _tensor("out[1]", out[1], k.shape, q)
-    q_, k_, qo, ko = _views(q, k, out[0], None if k is None else out[1])
-    _call("lact_rotary_fwd", q.device, stream, _byref(p), q_, k_, _at(freqs), _at(positions), _at(q_scale),
-          _at(q_offset), _at(k_scale), _at(k_offset), qo, ko)
+    _call("lact_rotary_fwd", q.device, stream, p, _view(q), _view(k), _at(freqs), _at(positions), _at(q_scale),
+          _at(q_offset), _at(k_scale), _at(k_offset), _view(out[0]), None if k is None else _view(out[1]))
     return out[0], (None if k is None else out[1])
 
 
@@ -214,15 +210,14 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
         if dk_out is not None:
             _tensor("k", k, dk_out.shape, dq_out)
             res["dk_scale"], res["dk_offset"] = torch.empty_like(k_scale), torch.empty_like(k_scale)
-        need = int(_abi.lib().lact_rotary_bwd_workspace_bytes(_byref(p)))
+        need = int(_abi.lib().lact_rotary_bwd_workspace_bytes(p))
         if need == 0:
             raise LactError(_abi.LACT_EINVAL, "lact_rotary_bwd_workspace_bytes")
         workspace = _workspace(workspace, need, dq_out.device)
-    gq, gk, q_, k_, dq, dk = _views(dq_out, dk_out, q if affine else None,
-                                    k if affine and dk_out is not None else None, res["dq"], res["dk"])
-    _call("lact_rotary_bwd", dq_out.device, stream, _byref(p), gq, gk, _at(freqs), _at(positions), q_, k_,
-          _at(q_scale), _at(k_scale), dq, dk, _at(res["dq_scale"]), _at(res["dq_offset"]), _at(res["dk_scale"]),
-          _at(res["dk_offset"]), _at(workspace) if affine else None, need)
+    _call("lact_rotary_bwd", dq_out.device, stream, p, _view(dq_out), _view(dk_out), _at(freqs), _at(positions),
+          _view(q) if affine else None, _view(k) if affine and dk_out is not None else None, _at(q_scale),
+          _at(k_scale), _view(res["dq"]), _view(res["dk"]), _at(res["dq_scale"]), _at(res["dq_offset"]),
+          _at(res["dk_scale"]), _at(res["dk_offset"]), _at(workspace) if affine else None, need)
     return res
 
 
@@ -241,8 +236,8 @@ def _swa_sink_problem(q, k, window, sinks, scale, T, Tq):
     B, H, _, d = q.shape
     if k.dim() != 4:
         raise ValueError("k must be a [B, Hkv, T, d] tensor")
-    return _abi.LactSwaSinkProblem(B, H, k.shape[1], T, Tq, d, int(window), int(sinks),
-                                   1.0 / math.sqrt(d) if scale is None else float(scale), _DT[q.dtype])
+    return _SINK(B, H, k.shape[1], T, Tq, d, int(window), int(sinks),
+                 1.0 / math.sqrt(d) if scale is None else float(scale), _DT[q.dtype])
 
 
 def _keys(q, k, v, lengths):
@@ -269,14 +264,13 @@ def swa_sink_fwd(q, k, v, window, sinks=0, *, lengths=None, scale=None, out=None
         lse = q.new_empty(q.shape[:3], dtype=torch.float32)
     else:
         _dense("lse", lse, q.shape[:3], torch.float32, q.device)
-    q_, k_, v_, o_ = _views(q, k, v, out)
-    _call("lact_swa_sink_fwd", q.device, stream, _byref(p), q_, k_, v_, _at(lengths), o_, _at(lse))
+    _call("lact_swa_sink_fwd", q.device, stream, p, _view(q), _view(k), _view(v), _at(lengths), _view(out), _at(lse))
     return out, lse
 
 
 def swa_sink_bwd_workspace_bytes(q, k, window, sinks=0) -> int:
     p = _swa_sink_problem(q, k, window, sinks, None, k.shape[2], q.shape[2])
-    return int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(_byref(p)))
+    return int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(p))
 
 
 def swa_sink_bwd(q, k, v, out, lse, dout, window, sinks=0, *, lengths=None, scale=None, dq=None, dk=None, dv=None,
@@ -293,13 +287,12 @@ def swa_sink_bwd(q, k, v, out, lse, dout, window, sinks=0, *, lengths=None, scal
     dq = _new(q) if dq is None else _tensor("dq", dq, q.shape, q)
     dk = _new(k) if dk is None else _tensor("dk", dk, k.shape, q)
     dv = _new(k) if dv is None else _tensor("dv", dv, k.shape, q)
-    need = int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(_byref(p)))
+    need = int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(p))
     if need == 0:
         raise LactError(_abi.LACT_EINVAL, "lact_swa_sink_bwd_workspace_bytes")
     workspace = _workspace(workspace, need, q.device)
-    q_, k_, v_, o_, g_, dq_, dk_, dv_ = _views(q, k, v, out, dout, dq, dk, dv)
-    _call("lact_swa_sink_bwd", q.device, stream, _byref(p), q_, k_, v_, o_, _at(lse), g_, _at(lengths), dq_, dk_, dv_,
-          _at(workspace), workspace.numel())
+    _call("lact_swa_sink_bwd", q.device, stream, p, _view(q), _view(k), _view(v), _view(out), _at(lse), _view(dout),
+          _at(lengths), _view(dq), _view(dk), _view(dv), _at(workspace), workspace.numel())
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -330,8 +323,8 @@ def swa_sink_decode(q, k, v, k_cache, v_cache, seen, window, sinks=0, *, scale=N
         out = _new(q)
     else:
         _tensor("out", out, q.shape, q)
-    q_, k_, v_, o_ = _views(q, k, v, out)
-    _call("lact_swa_sink_decode", q.device, stream, _byref(p), q_, k_, v_, _at(k_cache), _at(v_cache), _at(seen), o_)
+    _call("lact_swa_sink_decode", q.device, stream, p, _view(q), _view(k), _view(v), _at(k_cache), _at(v_cache),
+          _at(seen), _view(out))
     return out
 
 
@@ -344,5 +337,4 @@ def swa_cache_fill(k, v, k_cache, v_cache, window, sinks=0, *, lengths=None, str
     p = _swa_sink_problem(k, k, window, sinks, 1.0, T, 1)
     _keys(k, k, v, lengths)
     _caches(k, k, k_cache, v_cache, window, sinks)
-    k_, v_ = _views(k, v)
-    _call("lact_swa_cache_fill", k.device, stream, _byref(p), k_, v_, _at(lengths), _at(k_cache), _at(v_cache))
+    _call("lact_swa_cache_fill", k.device, stream, p, _view(k), _view(v), _at(lengths), _at(k_cache), _at(v_cache))

@@ -213,7 +213,7 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
         need = int(_abi.lib().lact_rotary_bwd_workspace_bytes(p))
         if need == 0:
             raise LactError(_abi.LACT_EINVAL, "lact_rotary_bwd_workspace_bytes")
-        workspace = _workspace(workspace, need, dq_out.device)
+        workspace = _workspace(workspace, need, dq_out.device, stream)
     _call("lact_rotary_bwd", dq_out.device, stream, p, _view(dq_out), _view(dk_out), _at(freqs), _at(positions),
           _view(q) if affine else None, _view(k) if affine and dk_out is not None else None, _at(q_scale),
           _at(k_scale), _view(res["dq"]), _view(res["dk"]), _at(res["dq_scale"]), _at(res["dq_offset"]),
@@ -221,9 +221,12 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
     return res
 
 
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, device, stream):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:   # it is dropped when the call returns, before that stream has used it
+            workspace.record_stream(stream)
+        return workspace
     if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the device of the call")
     if workspace.numel() < need:
@@ -290,7 +293,7 @@ def swa_sink_bwd(q, k, v, out, lse, dout, window, sinks=0, *, lengths=None, scal
     need = int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(p))
     if need == 0:
         raise LactError(_abi.LACT_EINVAL, "lact_swa_sink_bwd_workspace_bytes")
-    workspace = _workspace(workspace, need, q.device)
+    workspace = _workspace(workspace, need, q.device, stream)
     _call("lact_swa_sink_bwd", q.device, stream, p, _view(q), _view(k), _view(v), _view(out), _at(lse), _view(dout),
           _at(lengths), _view(dq), _view(dk), _view(dv), _at(workspace), workspace.numel())
     return {"dq": dq, "dk": dk, "dv": dv}

@@ -16,6 +16,9 @@ struct Extent4 {
   int64_t B, H, T, d;
 };
 
+// int32 and float32 arrays that are read singly (null: absent)
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 static bool view_ok(const lact_tensor4* t, const Extent4& e, int esz) {
   if (!t || !t->data || !aligned16(t->data)) return false;
   const int64_t s[3] = {t->stride_b, t->stride_h, t->stride_t}, n[3] = {e.B, e.H, e.T};
@@ -188,11 +191,21 @@ static int wattn_validate(const lact_swa_sink_problem* p, WattnDims& D) {
   D.DP = rup(p->d, 64);
   D.window = static_cast<int>(std::min(p->window, p->T));
   D.sinks = static_cast<int>(std::min(p->sinks, p->T));
+  if (static_cast<int64_t>(D.window) + D.sinks >= p->T) {   // no key is hidden: plain causal attention
+    D.window = static_cast<int>(p->T);
+    D.sinks = 0;
+  }
   D.dtype = p->dtype;
   D.bn = D.dtype == LACT_BF16 ? 128 : D.DP <= 128 ? SimtCfg<128>::kM : SimtCfg<256>::kM;
-  D.far_rows = D.dtype == LACT_BF16 ? kWattnFarRows : kWattnFarRowsF32;
   D.key_tiles = static_cast<int>(cdiv(D.T, D.bn));
   D.sink_tiles = static_cast<int>(cdiv(D.sinks, D.bn));
+  // far parts of kWattnFarRows query rows, fewer and longer where the sink tiles
+  // alone make four rounds of CTAs: each part's sums take workspace
+  D.far_rows = D.dtype == LACT_BF16 ? kWattnFarRows : kWattnFarRowsF32;
+  if (D.sink_tiles > 0) {
+    const int64_t most = std::max<int64_t>(1, 4 * kPlanSMs / (D.B * D.Hkv * D.sink_tiles));
+    D.far_rows = static_cast<int>(std::max<int64_t>(D.far_rows, rup(cdiv(D.T, most), 128)));
+  }
   const int far = far_parts(D.bn, D.window, static_cast<int>(D.T), D.far_rows);
   if (far == 0) D.sink_tiles = 0;   // the window reaches every query: no far part
   D.parts = 1 + far;
@@ -454,7 +467,7 @@ int lact_rotary_fwd(const lact_rotary_problem* p, const lact_tensor4* q, const l
   const int esz = p->dtype == LACT_BF16 ? 2 : 4;
   const Extent4 eq{p->B, p->H, p->T, p->d}, ek{p->B, p->Hkv, p->T, p->d};
   const bool has_k = p->Hkv > 0, affine = q_scale != nullptr;
-  if (!freqs || !aligned16(freqs) || !view_ok(q, eq, esz) || !view_ok(q_out, eq, esz)) return LACT_EINVAL;
+  if (!freqs || !aligned16(freqs) || !aligned4(positions) || !view_ok(q, eq, esz) || !view_ok(q_out, eq, esz)) return LACT_EINVAL;
   if (has_k && (!view_ok(k, ek, esz) || !view_ok(k_out, ek, esz))) return LACT_EINVAL;
   const float* params[] = {q_scale, q_offset, k_scale, k_offset};
   for (int i = 0; i < (has_k ? 4 : 2); ++i)
@@ -488,7 +501,7 @@ int lact_rotary_bwd(const lact_rotary_problem* p, const lact_tensor4* dq_out, co
   const int esz = p->dtype == LACT_BF16 ? 2 : 4;
   const Extent4 eq{p->B, p->H, p->T, p->d}, ek{p->B, p->Hkv, p->T, p->d};
   const bool has_k = p->Hkv > 0, affine = q_scale != nullptr;
-  if (!freqs || !aligned16(freqs) || !view_ok(dq_out, eq, esz) || !view_ok(dq, eq, esz)) return LACT_EINVAL;
+  if (!freqs || !aligned16(freqs) || !aligned4(positions) || !view_ok(dq_out, eq, esz) || !view_ok(dq, eq, esz)) return LACT_EINVAL;
   if (has_k && (!view_ok(dk_out, ek, esz) || !view_ok(dk, ek, esz))) return LACT_EINVAL;
   if (has_k && (k_scale != nullptr) != affine) return LACT_EINVAL;
   if (!aligned16(q_scale) || !aligned16(k_scale)) return LACT_EINVAL;
@@ -547,7 +560,7 @@ int lact_swa_sink_fwd(const lact_swa_sink_problem* p, const lact_tensor4* q, con
   const int esz = D.dtype == LACT_BF16 ? 2 : 4;
   const Extent4 eq{D.B, D.H, D.Tq, D.d}, ek{D.B, D.Hkv, D.T, D.d};
   if (!view_ok(q, eq, esz) || !view_ok(k, ek, esz) || !view_ok(v, ek, esz) || !view_ok(out, eq, esz)) return LACT_EINVAL;
-  if (!lse || !aligned16(lse)) return LACT_EINVAL;
+  if (!lse || !aligned4(lse) || !aligned4(lengths)) return LACT_EINVAL;
   WattnParams a = wattn_params(D, p->scale, lengths, lse);
   a.q = view4(q, eq); a.k = view4(k, ek); a.v = view4(v, ek); a.out = view4(out, eq);
   if (!injective(a.out, eq) || !apart(a.q, eq, a.out, eq, esz) || !apart(a.k, ek, a.out, eq, esz) ||
@@ -583,7 +596,7 @@ int lact_swa_sink_bwd(const lact_swa_sink_problem* p, const lact_tensor4* q, con
     if (!view_ok(x, eq, esz)) return LACT_EINVAL;
   for (const lact_tensor4* x : ks)
     if (!view_ok(x, ek, esz)) return LACT_EINVAL;
-  if (!lse || !aligned16(lse)) return LACT_EINVAL;
+  if (!lse || !aligned4(lse) || !aligned4(lengths)) return LACT_EINVAL;
   WattnParams a = wattn_params(D, p->scale, lengths, lse);
   a.q = view4(q, eq); a.k = view4(k, ek); a.v = view4(v, ek); a.out = view4(out, eq); a.dout = view4(dout, eq);
   a.dq = view4(dq, eq); a.dk = view4(dk, ek); a.dv = view4(dv, ek);
@@ -617,7 +630,7 @@ int lact_swa_sink_decode(const lact_swa_sink_problem* p, const lact_tensor4* q, 
   const int esz = p->dtype == LACT_BF16 ? 2 : 4;
   const Extent4 eq{p->B, p->H, 1, p->d}, ek{p->B, p->Hkv, 1, p->d};
   if (!view_ok(q, eq, esz) || !view_ok(out, eq, esz) || !view_ok(k, ek, esz) || !view_ok(v, ek, esz)) return LACT_EINVAL;
-  if (!seen || !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return LACT_EINVAL;
+  if (!seen || !aligned4(seen) || !k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return LACT_EINVAL;
   DecodeParams a;
   std::memset(&a, 0, sizeof(a));
   a.q = view4(q, eq); a.out = view4(out, eq); a.kn = view4(k, ek); a.vn = view4(v, ek);
@@ -647,7 +660,7 @@ int lact_swa_cache_fill(const lact_swa_sink_problem* p, const lact_tensor4* k, c
   if (p->T < 1 || p->T > (int64_t(1) << 24)) return LACT_EINVAL;
   const int esz = p->dtype == LACT_BF16 ? 2 : 4;
   const Extent4 ek{p->B, p->Hkv, p->T, p->d};
-  if (!view_ok(k, ek, esz) || !view_ok(v, ek, esz)) return LACT_EINVAL;
+  if (!view_ok(k, ek, esz) || !view_ok(v, ek, esz) || !aligned4(lengths)) return LACT_EINVAL;
   if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return LACT_EINVAL;
   FillParams a;
   std::memset(&a, 0, sizeof(a));

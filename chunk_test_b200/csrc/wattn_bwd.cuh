@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
         return true;
       };
       // a resident operand with the next tile of Y, by blocks
-      auto with_y = [&](uint32_t d, uint64_t a, int abuf) -> bool {
-        for (int kb = 0; kb < KB; ++kb, ++iy) {
+      auto with_y = [&](uint32_t d, uint64_t a, int abuf, int from, int to) -> bool {
+        for (int kb = from; kb < to; ++kb, ++iy) {
           const int s = iy % RY;
           if (!mbar_wait(&yfull[s], (iy / RY) & 1)) return false;
           tc_fence_after();
@@ -276,16 +276,27 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
       auto settle = [&]() {
         while (nt < p.nitems && (ncount = BwdItem<MODE>(p, nt).count) == 0) nt += gridDim.x;
       };
-      // dP (and S, where TMEM holds two) of the next tile; S alone
+      // dP (and S, where TMEM holds two) of the next tile, dP as far as Y's ring goes
+      constexpr int KD = DV || SB == 2 || RY >= KB ? KB : RY;
       auto next_d = [&]() -> bool {
         if (nn == 0 && !mbar_wait(&afull[ia % RA], (ia / RA) & 1)) return false;
         if constexpr (DV) {
-          if (!with_y(tmem + C::kColS + (h % SB) * 128, a1, ia % RA)) return false;
+          if (!with_y(tmem + C::kColS + (h % SB) * 128, a1, ia % RA, 0, KB)) return false;
           umma_commit(&sfull[h % SB]);
         } else {
           if (SB == 2 && !with_x(h, ia % RA)) return false;
           if (h > 0 && !mbar_wait(dread, (h - 1) & 1)) return false;   // the last dP has been read
-          if (!with_y(tmem + C::kColD, a2, ia % RA)) return false;
+          if (!with_y(tmem + C::kColD, a2, ia % RA, 0, KD)) return false;
+          if (KD == KB) umma_commit(dfull);
+        }
+        return true;
+      };
+      // The blocks of dP that the ring did not hold: they come while dX of the last
+      // tile is formed and X is refilled, instead of holding that dX up (dQ at d 256:
+      // 327 us, 306 with them so).
+      auto rest_of_d = [&]() -> bool {
+        if (KD < KB) {
+          if (!with_y(tmem + C::kColD, a2, ia % RA, KD, KB)) return false;
           umma_commit(dfull);
         }
         return true;
@@ -311,7 +322,7 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
         for (int n = 0; ok && n < t.count; ++n, ++g) {
           // tile g itself, as far as it could not be begun under the last one
           if (!begun && !next_d()) { ok = false; break; }
-          if (SB == 1 && !with_x(g, ia % RA)) { ok = false; break; }
+          if (SB == 1 && (!rest_of_d() || !with_x(g, ia % RA))) { ok = false; break; }
           if (SB == 1 || !begun) next_done();
           // the next one, where its resident operands can be there
           begun = nt < p.nitems && (RA == 2 || nn > 0);

@@ -428,7 +428,8 @@ int lact_rotary_bwd(const lact_rotary_problem* p, const lact_tensor4* dq_out, co
  * j <= i and (j > i - window or j < sinks) and both are below lengths[b]
  * (DEVICE [B] int32, clamped to 0..T; NULL: T).
  *   out_i = sum_j softmax_j(scale q_i . k_j) v_j      [B, H, Tq, d], dtype
- *   lse_i = log sum_j exp(scale q_i . k_j)            [B, H, Tq], float32
+ *   lse_i = log sum_j exp(scale q_i . k_j)            [B, H, Tq], float32,
+ *                                                     dense, 4-byte aligned
  * A row at or behind its sequence's length has out 0 and lse -inf, and what
  * k, v and q hold there is never used.  Values below the length have to be
  * finite: inside a tile a masked key's probability is 0, and 0 times an

@@ -180,3 +180,47 @@ def test_captured_and_replayed():
     assert torch.equal(y[0], want[0]) and torch.equal(y[1], want[1])
     for n in ref:
         assert torch.equal(res[n], ref[n]), n
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_queries_alone(dtype):
+    """No keys, with the scales' gradients: what q gets beside keys."""
+    q, k, g = inputs(2, 3, 2, 50, 64, dtype)
+    freqs, _ = ct.rotary_frequencies(32)
+    kw = params(3, 2, 64, g)
+    mine = {n: x for n, x in kw.items() if n.startswith("q")}
+    both, one = ct.rotary_fwd(q, k, freqs, **kw), ct.rotary_fwd(q, None, freqs, **mine)
+    assert torch.equal(both[0], one[0]) and one[1] is None
+    a = ct.rotary_bwd(q, k, freqs, q=both[0], k=both[1], **kw)
+    b = ct.rotary_bwd(q, None, freqs, q=both[0], **mine)
+    assert torch.equal(a["dq"], b["dq"]) and b["dk"] is None and b["dk_scale"] is None
+    # the tokens are cut differently: two 32-bit sums of 100 terms each, from the same terms
+    pos = torch.arange(50, device="cuda").expand(2, 50)
+    _, _, _, ads, ado = ao.rotary_vjp(q, freqs, pos, False, 1.0, both[0], kw["q_scale"])
+    assert bool(((a["dq_scale"] - b["dq_scale"]).abs() <= 2 * 100 * 2.0 ** -24 * 1.01 * ads).all())
+    assert bool(((a["dq_offset"] - b["dq_offset"]).abs() <= 2 * 100 * 2.0 ** -24 * 1.01 * ado).all())
+
+
+def test_refused_on_the_gpu():
+    q, k, g = inputs(1, 2, 1, 8, 64, torch.bfloat16)
+    freqs, _ = ct.rotary_frequencies(32)
+    kw = params(2, 1, 64, g)
+    want = ct.rotary_fwd(q, k, freqs)
+    with pytest.raises(ValueError):
+        ct.rotary_fwd(q, k, freqs.float())
+    with pytest.raises(ValueError):
+        ct.rotary_fwd(q, k, freqs, q_scale=kw["q_scale"])                 # all parameters or none
+    with pytest.raises(ValueError):
+        ct.rotary_fwd(q, None, freqs, **kw)                               # k's without k
+    with pytest.raises(ValueError):
+        ct.rotary_fwd(q, k, freqs, positions=torch.zeros((1, 8), device="cuda", dtype=torch.int64))
+    with pytest.raises(ValueError):
+        ct.rotary_bwd(q, k, freqs, q_scale=kw["q_scale"], k_scale=kw["k_scale"])   # the inputs are missing
+    with pytest.raises(ct.LactError):
+        ct.rotary_fwd(q, k, freqs, out=(k.expand(1, 2, 8, 64), k))        # heads on one place
+    with pytest.raises(ct.LactError):
+        ct.rotary_fwd(q, k, torch.ones(40, dtype=torch.float64, device="cuda"))    # 80 channels of 64
+    with pytest.raises(ct.LactError):
+        ct.rotary_fwd(q, k, freqs, start=-1)
+    got = ct.rotary_fwd(q, k, freqs)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

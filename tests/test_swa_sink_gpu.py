@@ -273,3 +273,65 @@ def test_refused_on_the_gpu():
     with pytest.raises(TypeError):
         ct.swa_sink_fwd(q.half(), k.half(), v.half(), 8, 1)
     assert torch.equal(ct.swa_sink_fwd(q, k, v, 8, 1)[0], out)   # and the next call is as good as the first
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_statistics_at_any_float_address(dtype):
+    """lse as a slice of a larger buffer, 4 bytes past a 16-byte boundary."""
+    q, k, v, dout = make(1, 1, 1, 131, 131, 64, dtype)
+    out, lse = ct.swa_sink_fwd(q, k, v, 20, 2)
+    part = torch.full((133,), 7.0, device="cuda")
+    at = part[1:132].view(1, 1, 131)
+    out2, _ = ct.swa_sink_fwd(q, k, v, 20, 2, lse=at)
+    assert torch.equal(out2, out) and torch.equal(at, lse) and float(part[0]) == 7 and float(part[-1]) == 7
+    a, b = (ct.swa_sink_bwd(q, k, v, out, x, dout, 20, 2) for x in (lse, at))
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,window,sinks", [(300, 100, 199), (300, 100, 200), (300, 1, 300), (300, 1, 10 ** 6),
+                                            (700, 1, 600), (300, 10 ** 9, 5)])
+def test_sinks_and_window_up_to_everything(T, window, sinks, dtype):
+    """Sinks over most of the sequence, one hidden key, none: causal attention."""
+    q, k, v, dout = make(1, 2, 1, T, T, 64, dtype)
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks)
+    w = ao.attention(q, k, v, window, sinks, dout=dout)
+    check_forward(out, lse, w, dtype, 64, T)
+    check_backward(ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks), w, dtype, 64, 2 * T)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_lengths_are_clamped(dtype):
+    q, k, v, dout = make(3, 1, 1, 150, 150, 64, dtype)
+    wide, tight = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ((10 ** 9, -7, 150), (150, 0, 150)))
+    a, b = (ct.swa_sink_fwd(q, k, v, 40, 2, lengths=x) for x in (wide, tight))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga, gb = (ct.swa_sink_bwd(q, k, v, *a, dout, 40, 2, lengths=x) for x in (wide, tight))
+    for n in ga:
+        assert torch.equal(ga[n], gb[n]), n
+
+
+def test_workspace_stays_bounded_with_many_sinks():
+    """Half of a long sequence as sinks: the parts' sums are a few per tile."""
+    q = torch.empty((1, 1, 32768, 256), dtype=BF16, device="cuda")
+    need = ct.swa_sink_bwd_workspace_bytes(q, q, 64, 16384)
+    assert need <= 32768 * 4 + 128 * 6 * 2 * 128 * 256 * 4 + 512, need
+
+
+def test_own_stream_without_a_workspace():
+    """stream= alone: the workspace that the call makes lives until that stream is done with it."""
+    q, k, v, dout = make(1, 2, 1, 3000, 3000, 128, BF16)
+    out, lse = ct.swa_sink_fwd(q, k, v, 200, 4)
+    want = ct.swa_sink_bwd(q, k, v, out, lse, dout, 200, 4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        got.append(ct.swa_sink_bwd(q, k, v, out, lse, dout, 200, 4, stream=side))
+        for _ in range(3):   # what would take the dropped workspace on the current stream
+            torch.full((ct.swa_sink_bwd_workspace_bytes(q, k, 200, 4),), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for g in got:
+        for n in g:
+            assert torch.equal(g[n], want[n]), n

@@ -387,15 +387,13 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
             x = mycol < 128 ? p.a.lse[at] * -1.4426950408889634f : -p.a.delta[at];
           }
         }
-        float dp[BOTH ? 32 : 64];
-        if (BOTH) {
-          if (!mbar_wait_warp(dfull, g & 1)) { ok = false; break; }
-        } else if (!DV) {
+        float dp[64];
+        if (!DV) {
           // dP first, so that its buffer is free while dS is computed
           if (!mbar_wait_warp(dfull, g & 1)) { ok = false; break; }
           tc_fence_after();
           tmem_ld32(td, dp);
-          tmem_ld32(td + 32, dp + (BOTH ? 0 : 32));
+          tmem_ld32(td + 32, dp + 32);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
@@ -445,8 +443,6 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
 #pragma unroll
           for (int c = 0; c < 32; ++c) hw[c] = 0;
           if (BOTH) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dread);
             tmem_st16u(ts, hw);
             tmem_st16u(ts + 16, hw);
             tmem_st16u(ts + 32, hw);
@@ -457,13 +453,7 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
         for (int c0 = 0; c0 < 64; c0 += 32) {
           float s[32];
           tmem_ld32(ts + c0, s);
-          if (BOTH) tmem_ld32(td + c0, dp);
           tmem_ld_wait();
-          if (BOTH && c0 == 32) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dread);
-          }
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
             float4 l4 = make_float4(rl, rl, rl, rl), d4 = make_float4(rd, rd, rd, rd);
@@ -479,14 +469,14 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
               float2 e = fma_f32x2(make_float2(s[c + k], s[c + k + 1]), make_float2(c2, c2), ll[k / 2]);
               e.x = ex2_approx(e.x);
               e.y = ex2_approx(e.y);
-              const int d = (BOTH ? 0 : c0) + c + k;
+              const int d = c0 + c + k;
               if (BOTH) {
                 s[c + k] = e.x;
                 s[c + k + 1] = e.y;
               }
               if (!DV) e = mul_f32x2(e, add_f32x2(make_float2(dp[d], dp[d + 1]), dd[k / 2]));
-              (BOTH ? dp : s)[c + k] = e.x;
-              (BOTH ? dp : s)[c + k + 1] = e.y;
+              (BOTH ? dp[d] : s[c + k]) = e.x;
+              (BOTH ? dp[d + 1] : s[c + k + 1]) = e.y;
             }
           }
           if (!whole) {
@@ -495,14 +485,14 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
             for (int c = 0; c < 32; ++c)
               if (!(see >> c & 1)) {
                 s[c] = 0.f;
-                if (BOTH) dp[c] = 0.f;
+                if (BOTH) dp[c0 + c] = 0.f;
               }
           }
           // the last product's operand: half a step, 2^-8 of each
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             hw[(BOTH ? 0 : c0 / 2) + c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
-            if (BOTH) hw[16 + c] = pack_bf16x2(dp[2 * c], dp[2 * c + 1]);
+            if (BOTH) hw[16 + c] = pack_bf16x2(dp[c0 + 2 * c], dp[c0 + 2 * c + 1]);
           }
           if (BOTH) {   // P and dS over the 32 columns that this thread has read
             tmem_st16u(ts + c0, hw);

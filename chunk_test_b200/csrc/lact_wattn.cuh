@@ -109,8 +109,9 @@ static int rotary_validate(const lact_rotary_problem* p) {
 }
 
 // Vectors of 4 channels where both halves of a pair start on one (interleaved
-// pairs: of 16 bytes), else single channels.  A block takes as many heads as 384 threads (512 where a head alone
-// has more units) hold, so angles are formed once for all of them.
+// pairs: of 16 bytes), else single channels.  A block takes as many heads as 384
+// threads (512 where a head alone has more units) hold, so angles are formed once
+// for all of them.
 static RotaryDims rotary_dims(const lact_rotary_problem* p, bool sums) {
   RotaryDims r;
   const int d = static_cast<int>(p->d), rot = static_cast<int>(p->rot);

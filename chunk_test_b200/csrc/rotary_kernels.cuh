@@ -50,12 +50,9 @@ struct RotaryParams {
 
 template <int V>
 __device__ __forceinline__ void load_vec(const float* p, float* x) {
-  if constexpr (V == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-  } else {
-    x[0] = *p;
-  }
+  static_assert(V == 4, "16 bytes");
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
 template <int V>
 __device__ __forceinline__ void store_vec(float* p, const float* x) {
@@ -64,16 +61,13 @@ __device__ __forceinline__ void store_vec(float* p, const float* x) {
 }
 template <int V>
 __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float* x) {
-  if constexpr (V == 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  static_assert(V == 8, "16 bytes");
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    x[0] = __bfloat162float(*p);
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 // the one rounding of a bf16 result: to nearest, ties to even

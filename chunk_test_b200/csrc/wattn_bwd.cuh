@@ -26,15 +26,23 @@
 // Bound by latency: up to d = 128 by the elementwise work of a tile (16384
 // exponentials, 1024 clocks, and as many differences and products), which the
 // passes of 9 tiles repeat; at d = 256 by the chain S, dS, dX of one tile (about
-// 5000 clocks for 3072 of products), for TMEM holds one S beside 256 columns of
+// 5400 clocks for 3 x 1024 of products), for TMEM holds one S beside 256 columns of
 // dX, and shared memory one B1.  Measured: B 2, H 6, T 8192, d 256, window 2048,
-// 4 sinks: dQ 327 us, dK and dV 580; B 2, 12 heads on 4, T 4001, d 128, window
-// 1000, 8 sinks: 103 and 174.
+// 4 sinks: dQ 306 us, dK and dV 554; B 2, 12 heads on 4, T 4001, d 128, window
+// 1000, 8 sinks: 103 and 173.
 #pragma once
 
 #include "wattn_fwd.cuh"
 
 namespace lact {
+
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
 
 enum WattnMode { WATTN_DQ, WATTN_DK, WATTN_DV, WATTN_DKV };   // DKV: d <= 128
 
@@ -450,55 +458,55 @@ __global__ void __launch_bounds__(352, 1) k_wattn_bwd(const __grid_constant__ Wa
           }
         } else {
 #pragma unroll
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          float s[32];
-          tmem_ld32(ts + c0, s);
-          tmem_ld_wait();
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            float s[32];
+            tmem_ld32(ts + c0, s);
+            tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            float4 l4 = make_float4(rl, rl, rl, rl), d4 = make_float4(rd, rd, rd, rd);
-            if (MODE != WATTN_DQ) {
-              asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(l4.x), "=f"(l4.y), "=f"(l4.z), "=f"(l4.w) : "r"(col_s + (c0 + c) * 4));
-              if (!DV)
-                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(d4.x), "=f"(d4.y), "=f"(d4.z), "=f"(d4.w) : "r"(col_s + 512 + (c0 + c) * 4));
-            }
-            const float2 ll[2] = {make_float2(l4.x, l4.y), make_float2(l4.z, l4.w)};
-            const float2 dd[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              float2 e = fma_f32x2(make_float2(s[c + k], s[c + k + 1]), make_float2(c2, c2), ll[k / 2]);
-              e.x = ex2_approx(e.x);
-              e.y = ex2_approx(e.y);
-              const int d = c0 + c + k;
-              if (BOTH) {
-                s[c + k] = e.x;
-                s[c + k + 1] = e.y;
+            for (int c = 0; c < 32; c += 4) {
+              float4 l4 = make_float4(rl, rl, rl, rl), d4 = make_float4(rd, rd, rd, rd);
+              if (MODE != WATTN_DQ) {
+                l4 = ld_shared_v4(col_s + (c0 + c) * 4);
+                if (!DV)
+                  d4 = ld_shared_v4(col_s + 512 + (c0 + c) * 4);
               }
-              if (!DV) e = mul_f32x2(e, add_f32x2(make_float2(dp[d], dp[d + 1]), dd[k / 2]));
-              (BOTH ? dp[d] : s[c + k]) = e.x;
-              (BOTH ? dp[d + 1] : s[c + k + 1]) = e.y;
+              const float2 ll[2] = {make_float2(l4.x, l4.y), make_float2(l4.z, l4.w)};
+              const float2 dd[2] = {make_float2(d4.x, d4.y), make_float2(d4.z, d4.w)};
+#pragma unroll
+              for (int k = 0; k < 4; k += 2) {
+                float2 e = fma_f32x2(make_float2(s[c + k], s[c + k + 1]), make_float2(c2, c2), ll[k / 2]);
+                e.x = ex2_approx(e.x);
+                e.y = ex2_approx(e.y);
+                const int d = c0 + c + k;
+                if (BOTH) {
+                  s[c + k] = e.x;
+                  s[c + k + 1] = e.y;
+                }
+                if (!DV) e = mul_f32x2(e, add_f32x2(make_float2(dp[d], dp[d + 1]), dd[k / 2]));
+                (BOTH ? dp[d] : s[c + k]) = e.x;
+                (BOTH ? dp[d + 1] : s[c + k + 1]) = e.y;
+              }
+            }
+            if (!whole) {
+              const uint32_t see = visible_bits(clo, chi, csk, c0);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(see >> c & 1)) {
+                  s[c] = 0.f;
+                  if (BOTH) dp[c0 + c] = 0.f;
+                }
+            }
+            // the last product's operand: half a step, 2^-8 of each
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              hw[(BOTH ? 0 : c0 / 2) + c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
+              if (BOTH) hw[16 + c] = pack_bf16x2(dp[c0 + 2 * c], dp[c0 + 2 * c + 1]);
+            }
+            if (BOTH) {   // P and dS over the 32 columns that this thread has read
+              tmem_st16u(ts + c0, hw);
+              tmem_st16u(ts + c0 + 16, hw + 16);
             }
           }
-          if (!whole) {
-            const uint32_t see = visible_bits(clo, chi, csk, c0);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(see >> c & 1)) {
-                s[c] = 0.f;
-                if (BOTH) dp[c0 + c] = 0.f;
-              }
-          }
-          // the last product's operand: half a step, 2^-8 of each
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            hw[(BOTH ? 0 : c0 / 2) + c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
-            if (BOTH) hw[16 + c] = pack_bf16x2(dp[c0 + 2 * c], dp[c0 + 2 * c + 1]);
-          }
-          if (BOTH) {   // P and dS over the 32 columns that this thread has read
-            tmem_st16u(ts + c0, hw);
-            tmem_st16u(ts + c0 + 16, hw + 16);
-          }
-        }
         }
         // over the first half of the 64 columns that this thread has read
         if (!BOTH) {

@@ -37,7 +37,7 @@ __device__ __forceinline__ int seq_len(const WattnParams& p, int b) {
 // window's tiles see fewer keys).  heads_first: all heads at one position
 // together, so that those short tiles make the last round: for few rounds (the
 // dQ of 768 tiles on 148 SMs: 324 us, 362 head by head).  Else head by head, whose
-// CTAs share keys in L2 (the forward of 3072 tiles: 718 us, 752 the other way).
+// CTAs share keys in L2 (the forward of 24 times 128 tiles: 718 us, 752 the other way).
 struct TileAt {
   int b, h, m;
 };

@@ -4,8 +4,8 @@
 //
 // Tiles of 32 rows (64 above d = 128) against tiles of 32 in shared memory, 4
 // threads a row; small tiles, so that a short sequence fills more SMs, as long as
-// two CTAs or more share one.  A thread holds 4 x 2 scores and 4 rows x (D/16) columns of each product that runs
-// over the other axis.  Bound by latency where
+// two CTAs or more share one.  A thread holds 4 x 2 scores and 4 rows x (D/16)
+// columns of each product that runs over the other axis.  Bound by latency where
 // there are few CTAs (B 1, H 4, T 1025, d 64, window 256: dQ 54 us, dK and dV 58),
 // else by the FP32 pipe and the shared-memory reads that feed it.
 #pragma once

@@ -173,6 +173,7 @@ static RotaryParams rotary_params(const lact_rotary_problem* p, const RotaryDims
 // Query rows of a sink tile's far part: about the work of a near part; the
 // CUDA cores take as long for a quarter of the rows.
 constexpr int kWattnFarRows = 1024, kWattnFarRowsF32 = 256;
+constexpr int kWalkedSequences = 32;  // a tile's place is found in about 20 clocks a sequence
 constexpr int kFewRounds = 8;         // rounds of persistent CTAs below which the short tiles go last
 
 struct WattnDims {
@@ -234,6 +235,7 @@ static WattnParams wattn_params(const WattnDims& D, float scale, const int32_t* 
   a.B = static_cast<int>(D.B); a.H = static_cast<int>(D.H); a.Hkv = static_cast<int>(D.Hkv);
   a.group = static_cast<int>(D.H / D.Hkv); a.T = static_cast<int>(D.T); a.Tq = static_cast<int>(D.Tq);
   a.d = static_cast<int>(D.d); a.window = D.window; a.sinks = D.sinks; a.far_rows = D.far_rows;
+  a.by_length = lengths != nullptr && D.B <= kWalkedSequences;
   return a;
 }
 

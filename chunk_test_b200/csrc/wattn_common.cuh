@@ -24,7 +24,7 @@ struct WattnParams {
   int B, H, Hkv, group, T, Tq, d;    // group = H / Hkv
   int window, sinks;                 // each at most T
   int far_rows;                      // query rows of one far part of a sink tile
-  int heads_first;                   // order of the query tiles (query_tile_at)
+  int heads_first, by_length;        // order of the query tiles (query_tile_at)
 };
 
 __device__ __forceinline__ int seq_len(const WattnParams& p, int b) {
@@ -32,8 +32,9 @@ __device__ __forceinline__ int seq_len(const WattnParams& p, int b) {
 }
 
 // The v-th query tile of 128 rows in the order in which persistent CTAs take
-// them: first the tiles that hold tokens, then the tiles behind the lengths,
-// which are only filled; the later positions of a sequence first (the first
+// them.  by_length (a few sequences, for their lengths are walked): first the tiles
+// that hold tokens, then the tiles behind the lengths, which are only filled; else
+// sequence after sequence.  The later positions of a sequence first (the first
 // window's tiles see fewer keys).  heads_first: all heads at one position
 // together, so that those short tiles make the last round: for few rounds (the
 // dQ of 768 tiles on 148 SMs: 324 us, 362 head by head).  Else head by head, whose
@@ -46,9 +47,8 @@ __device__ __forceinline__ TileAt query_tile_at(const WattnParams& p, int nb, in
   const int off = p.T - p.Tq;
   for (int behind = 0; behind < 2; ++behind)
     for (t.b = 0; t.b < p.B; ++t.b) {
-      // without lengths: every sequence alike, none behind
-      const int some = p.lengths ? min(nb, (max(seq_len(p, t.b) - off, 0) + 127) >> 7) : nb;
-      if (!p.lengths) {
+      const int some = p.by_length ? min(nb, (max(seq_len(p, t.b) - off, 0) + 127) >> 7) : nb;
+      if (!p.by_length) {   // every sequence alike
         t.b = v / (nb * p.H);
         v %= nb * p.H;
       }

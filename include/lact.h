@@ -455,7 +455,8 @@ size_t lact_swa_sink_bwd_workspace_bytes(const lact_swa_sink_problem* p);
 /* Its backward: the gradients dq, dk, dv (dtype) for the gradient `dout` of
  * out, from the forward's inputs, out and lse.  No atomics: the same bits on
  * every run.  Rows behind a sequence's length get 0.  `workspace`: device
- * scratch, 256-byte aligned. */
+ * scratch, 256-byte aligned, the call's alone until the stream reaches its end
+ * (two captured graphs that share one may not run at once). */
 int lact_swa_sink_bwd(const lact_swa_sink_problem* p, const lact_tensor4* q, const lact_tensor4* k,
                       const lact_tensor4* v, const lact_tensor4* out, const float* lse,
                       const lact_tensor4* dout, const int32_t* lengths,

@@ -335,3 +335,16 @@ def test_own_stream_without_a_workspace():
     for g in got:
         for n in g:
             assert torch.equal(g[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B", [31, 70])
+def test_many_ragged_sequences(B, dtype):
+    T, window, sinks = 150, 40, 3
+    lengths = [(37 * b) % (T + 1) for b in range(B)]
+    q, k, v, dout = make(B, 2, 1, T, T, 64, dtype)
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lens)
+    w = ao.attention(q, k, v, window, sinks, lengths, dout=dout)
+    check_forward(out, lse, w, dtype, 64, window + sinks)
+    check_backward(ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks, lengths=lens), w, dtype, 64, 2 * T)

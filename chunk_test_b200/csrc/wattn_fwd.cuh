@@ -499,10 +499,13 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
         ++tc;
         tc_fence_after();
       }
-      // rows of 64 bytes in 64-byte swizzle; rows and channels outside are clipped by the store
+      // rows of 64 bytes in 64-byte swizzle; rows and channels outside are clipped by the store.
+      // A warp without a row below Tq stages nothing: each step that writes a staging tile also
+      // commits a group, which the wait below counts on.
+      const int channels = t.q0 + quarter * 32 < p.a.Tq ? p.a.d : 0;
       const uint32_t stage = smem_u32(smem + C::kOffStage) + (warp - 2) * C::kStages * 2048;
 #pragma unroll 1
-      for (int c0 = 0; c0 < p.a.d; c0 += 32, ++nst) {
+      for (int c0 = 0; c0 < channels; c0 += 32, ++nst) {
         float o[32];
         if (t.count > 0) {
           __syncwarp();
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(WattnCfg<D>::kThreads, WattnCfg<D>::kCtas)
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0 && t.q0 + quarter * 32 < p.a.Tq) {
+        if (lane == 0) {
           tma_store_4d(&p.tmO, to, c0, t.q0 + quarter * 32, t.h, t.b);
           bulk_commit_group();
         }

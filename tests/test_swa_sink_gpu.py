@@ -348,3 +348,23 @@ def test_many_ragged_sequences(B, dtype):
     w = ao.attention(q, k, v, window, sinks, lengths, dout=dout)
     check_forward(out, lse, w, dtype, 64, window + sinks)
     check_backward(ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks, lengths=lens), w, dtype, 64, 2 * T)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_ragged_tiles_whose_last_rows_are_missing(d):
+    """Several query tiles per CTA, the last of each head with rows for some of
+    its warps only (40 and 8 of 128), and tiles wholly behind their sequence's
+    length right after tiles with tokens: every row, several times over."""
+    H, Hkv, window, sinks = 12, 4, 100, 4
+    for T in (7 * 128 + 40, 7 * 128 + 8):
+        lengths = [T if b % 3 == 0 else (97 * b) % T for b in range(14)]     # 1344 tiles
+        q, k, v, _ = make(14, H, Hkv, T, T, d, BF16, "bthd", seed=T)
+        lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        w = ao.attention(q, k, v, window, sinks, lengths)
+        first = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lens)
+        check_forward(*first, w, BF16, d, window + sinks)
+        for _ in range(10):
+            out = torch.full_like(first[0], 7.0)
+            again = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lens, out=out)
+            assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    assert ct.status() == ct.LACT_OK

@@ -6,7 +6,8 @@ Tensors are [B, heads, T, d] CUDA tensors in bf16 or float32 whose channels
 are contiguous; the other strides are free (multiples of 16 bytes), so a
 projection's [B, T, heads, d] result is passed as its transpose, and outputs
 given by the caller may have that layout too.  Calls run on the tensors'
-device, on torch's current stream there (or `stream=`).
+device, on torch's current stream there (or `stream=`, from whose pool they
+then make their results and workspaces).
 """
 from __future__ import annotations
 
@@ -36,9 +37,28 @@ def _view(t):
     return _TENSOR(t.data_ptr(), s[0], s[1], s[2])
 
 
-def _new(t):
-    """A new contiguous tensor like `t`."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+def _made(stream, make, *args, **kw):
+    """make(*args, **kw), a new tensor for a call on `stream` (None: the current
+    one).  It comes from that stream's pool: a block that another stream's pool
+    hands out may still be in use there by what was queued before."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _result(stream, make, *args, **kw):
+    """_made, for a tensor that the caller gets and may read on the current
+    stream: it is recorded there, so that its block is not reused before."""
+    t = _made(stream, make, *args, **kw)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _new(t, stream):
+    """A new contiguous result like `t`."""
+    return _result(stream, torch.empty_like, t, memory_format=torch.contiguous_format)
 
 
 def _at(t):
@@ -172,7 +192,7 @@ def rotary_fwd(q, k, freqs, *, positions=None, start=0, interleaved=False, ampli
     p = _rotary_args(q, k, freqs, positions, start, interleaved, amplitude)
     _params(("q_scale", "q_offset", "k_scale", "k_offset"), (q_scale, q_offset, k_scale, k_offset), q, k)
     if out is None:
-        out = (_new(q), None if k is None else _new(k))
+        out = (_new(q, stream), None if k is None else _new(k, stream))
     else:
         _tensor("out[0]", out[0], q.shape, q)
         if k is not None:
@@ -194,9 +214,9 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
     affine = _params(("q_scale", "k_scale"), (q_scale, k_scale), dq_out, dk_out)
     res = dict.fromkeys(("dq", "dk", "dq_scale", "dq_offset", "dk_scale", "dk_offset"))
     if out is None:
-        res["dq"] = _new(dq_out)
+        res["dq"] = _new(dq_out, stream)
         if dk_out is not None:
-            res["dk"] = _new(dk_out)
+            res["dk"] = _new(dk_out, stream)
     else:
         res["dq"] = _tensor("out[0]", out[0], dq_out.shape, dq_out)
         if dk_out is not None:
@@ -206,10 +226,10 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
         if q is None or (dk_out is not None and k is None):
             raise ValueError("the scales' gradients need the forward's q and k")
         _tensor("q", q, dq_out.shape, dq_out)
-        res["dq_scale"], res["dq_offset"] = torch.empty_like(q_scale), torch.empty_like(q_scale)
+        res["dq_scale"], res["dq_offset"] = _new(q_scale, stream), _new(q_scale, stream)
         if dk_out is not None:
             _tensor("k", k, dk_out.shape, dq_out)
-            res["dk_scale"], res["dk_offset"] = torch.empty_like(k_scale), torch.empty_like(k_scale)
+            res["dk_scale"], res["dk_offset"] = _new(k_scale, stream), _new(k_scale, stream)
         need = int(_abi.lib().lact_rotary_bwd_workspace_bytes(p))
         if need == 0:
             raise LactError(_abi.LACT_EINVAL, "lact_rotary_bwd_workspace_bytes")
@@ -223,10 +243,7 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
 
 def _workspace(workspace, need, device, stream):
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:   # it is dropped when the call returns, before that stream has used it
-            workspace.record_stream(stream)
-        return workspace
+        return _made(stream, torch.empty, need, dtype=torch.uint8, device=device)
     if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the device of the call")
     if workspace.numel() < need:
@@ -260,11 +277,11 @@ def swa_sink_fwd(q, k, v, window, sinks=0, *, lengths=None, scale=None, out=None
     p = _swa_sink_problem(q, k, window, sinks, scale, k.shape[2], q.shape[2])
     _keys(q, k, v, lengths)
     if out is None:
-        out = _new(q)
+        out = _new(q, stream)
     else:
         _tensor("out", out, q.shape, q)
     if lse is None:
-        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+        lse = _result(stream, torch.empty, q.shape[:3], dtype=torch.float32, device=q.device)
     else:
         _dense("lse", lse, q.shape[:3], torch.float32, q.device)
     _call("lact_swa_sink_fwd", q.device, stream, p, _view(q), _view(k), _view(v), _at(lengths), _view(out), _at(lse))
@@ -287,9 +304,9 @@ def swa_sink_bwd(q, k, v, out, lse, dout, window, sinks=0, *, lengths=None, scal
     _tensor("out", out, q.shape, q)
     _tensor("dout", dout, q.shape, q)
     _dense("lse", lse, q.shape[:3], torch.float32, q.device)
-    dq = _new(q) if dq is None else _tensor("dq", dq, q.shape, q)
-    dk = _new(k) if dk is None else _tensor("dk", dk, k.shape, q)
-    dv = _new(k) if dv is None else _tensor("dv", dv, k.shape, q)
+    dq = _new(q, stream) if dq is None else _tensor("dq", dq, q.shape, q)
+    dk = _new(k, stream) if dk is None else _tensor("dk", dk, k.shape, q)
+    dv = _new(k, stream) if dv is None else _tensor("dv", dv, k.shape, q)
     need = int(_abi.lib().lact_swa_sink_bwd_workspace_bytes(p))
     if need == 0:
         raise LactError(_abi.LACT_EINVAL, "lact_swa_sink_bwd_workspace_bytes")
@@ -323,7 +340,7 @@ def swa_sink_decode(q, k, v, k_cache, v_cache, seen, window, sinks=0, *, scale=N
     _caches(q, k, k_cache, v_cache, window, sinks)
     _dense("seen", seen, (B,), torch.int32, q.device)
     if out is None:
-        out = _new(q)
+        out = _new(q, stream)
     else:
         _tensor("out", out, q.shape, q)
     _call("lact_swa_sink_decode", q.device, stream, p, _view(q), _view(k), _view(v), _at(k_cache), _at(v_cache),

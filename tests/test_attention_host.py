@@ -254,3 +254,57 @@ def test_oracle_decode_follows_the_sequence():
     for t in range(T):
         o, _, kc, vc = ao.decode(q[:, :, t:t + 1], k[:, :, t:t + 1], v[:, :, t:t + 1], kc, vc, [t], window, sinks)
         assert torch.allclose(o, want[:, :, t:t + 1], rtol=1e-12, atol=1e-14)
+
+
+def test_own_stream_makes_its_tensors_there(monkeypatch):
+    """With stream= the results and workspaces come from that stream's pool (the
+    current stream's may hand out a block whose last users are still queued),
+    and the results are recorded on the current stream.  Without a GPU: the
+    library is not called, and streams are names."""
+    from chunk_test_b200 import attention as at
+    current, made, recorded = ["main"], [], []
+
+    class Stream:
+        cuda_stream = 0
+
+        def __enter__(self):
+            current.append("side")
+
+        def __exit__(self, *a):
+            current.pop()
+
+    def tracked(make):
+        def call(*args, **kw):
+            t = make(*args, **kw)
+            made.append((t.data_ptr(), current[-1]))
+            return t
+        return call
+
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)))
+    monkeypatch.setattr(torch.Tensor, "new_empty", tracked(torch.Tensor.new_empty))
+    for name in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, name, tracked(getattr(torch, name)))
+    monkeypatch.setattr(at, "_query", lambda q: None)
+    monkeypatch.setattr(at, "_dense", lambda name, t, *a: t)
+    monkeypatch.setattr(at, "_call", lambda *a: None)
+    q, k = torch.zeros(2, 4, 600, 64), torch.zeros(2, 2, 600, 64)
+    one, key = q[:, :, :1], k[:, :, :1]
+    kc, vc = torch.zeros(2, 2, 8, 64), torch.zeros(2, 2, 8, 64)
+    lse, freqs, scale = torch.zeros(2, 4, 600), torch.ones(32, dtype=torch.float64), torch.ones(4, 64)
+    side = Stream()
+    calls = {
+        "rotary_fwd": (2, 0, lambda: ct.rotary_fwd(q, k, freqs, stream=side)),
+        "rotary_bwd": (6, 1, lambda: ct.rotary_bwd(q, k, freqs, q=q, k=k, q_scale=scale, k_scale=scale[:2], stream=side)),
+        "fwd": (2, 0, lambda: ct.swa_sink_fwd(q, k, k, 8, 2, stream=side)),
+        "bwd": (3, 1, lambda: ct.swa_sink_bwd(q, k, k, q, lse, q, 8, 2, stream=side)),
+        "decode": (1, 0, lambda: ct.swa_sink_decode(one, key, key, kc, vc, lse, 6, 2, stream=side)),
+    }
+    for name, (results, workspaces, call) in calls.items():
+        made.clear(), recorded.clear()
+        kept = call()
+        assert len(made) == results + workspaces, name
+        assert all(where == "side" for _, where in made), name
+        got = [x for x in (kept.values() if isinstance(kept, dict) else kept if isinstance(kept, tuple) else [kept])]
+        assert sorted(x.data_ptr() for x in got) == sorted(p for p, s in recorded if s == "main"), name

@@ -368,3 +368,22 @@ def test_many_ragged_tiles_whose_last_rows_are_missing(d):
             again = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lens, out=out)
             assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
     assert ct.status() == ct.LACT_OK
+
+
+def test_own_stream_takes_no_block_in_use():
+    """A backward on the current stream and, at once, one on another stream whose
+    inputs are there: the second does not take the first one's workspace, which
+    went back to the current stream's pool while the first still runs."""
+    cases = [make(1, 4, 2, 6000, 6000, 128, BF16, seed=s) for s in (1, 2)]
+    fwd = [ct.swa_sink_fwd(q, k, v, 1000, 4) for q, k, v, _ in cases]
+    alone = [ct.swa_sink_bwd(q, k, v, *f, g, 1000, 4) for (q, k, v, g), f in zip(cases, fwd)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for (q, k, v, g), f, s in zip(cases, fwd, (None, side)):
+            got.append(ct.swa_sink_bwd(q, k, v, *f, g, 1000, 4, stream=s))
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            for n in a:
+                assert torch.equal(a[n], b[n]), n

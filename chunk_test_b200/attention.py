@@ -18,6 +18,7 @@ import torch
 
 from . import _abi
 from ._abi import LactError
+from .layer import _made, _result
 
 _DT = {torch.float32: _abi.LACT_F32, torch.bfloat16: _abi.LACT_BF16}
 
@@ -35,25 +36,6 @@ def _view(t):
         return None
     s = t.stride()
     return _TENSOR(t.data_ptr(), s[0], s[1], s[2])
-
-
-def _made(stream, make, *args, **kw):
-    """make(*args, **kw), a new tensor for a call on `stream` (None: the current
-    one).  It comes from that stream's pool: a block that another stream's pool
-    hands out may still be in use there by what was queued before."""
-    if stream is None:
-        return make(*args, **kw)
-    with torch.cuda.stream(stream):
-        return make(*args, **kw)
-
-
-def _result(stream, make, *args, **kw):
-    """_made, for a tensor that the caller gets and may read on the current
-    stream: it is recorded there, so that its block is not reused before."""
-    t = _made(stream, make, *args, **kw)
-    if stream is not None:
-        t.record_stream(torch.cuda.current_stream(t.device))
-    return t
 
 
 def _new(t, stream):

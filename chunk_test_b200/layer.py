@@ -22,6 +22,25 @@ def _ptr(t):
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
 
 
+def _made(stream, make, *args, **kw):
+    """make(*args, **kw), a new tensor for a call on `stream` (None: the current
+    one).  It comes from that stream's pool: a block that another stream's pool
+    hands out may still be in use there by what was queued before."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _result(stream, make, *args, **kw):
+    """_made, for a tensor that the caller gets and may read on the current
+    stream: it is recorded there, so that its block is not reused before."""
+    t = _made(stream, make, *args, **kw)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def make_problem(q, k, w1, chunk, order, rule) -> _abi.LactProblem:
     B, H, Tq, d = q.shape
     T = k.shape[2]
@@ -216,17 +235,16 @@ def ttt_fwd(q, k, v, lr, beta, w1, w2, w3, chunk, order, rule, *, out=None, w_ou
     B, H, Tq, d = q.shape
     dh = w1.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     if w_out is None:
-        w_out = (torch.empty((B * H, dh, d), device=q.device, dtype=torch.float32),
-                 torch.empty((B * H, d, dh), device=q.device, dtype=torch.float32),
-                 torch.empty((B * H, dh, d), device=q.device, dtype=torch.float32))
+        w_out = tuple(_result(stream, torch.empty, (B * H, *s), device=q.device, dtype=torch.float32)
+                      for s in ((dh, d), (d, dh), (dh, d)))
     _check_outputs(q, w1, out, w_out, "cuda")
     need = _abi.workspace_bytes(p)
     if need == 0:
         raise LactError(_abi.LACT_EINVAL, "lact_ttt_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _made(stream, torch.empty, need, device=q.device, dtype=torch.uint8)
     _check_workspace(workspace, q.device, need)
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
@@ -288,27 +306,26 @@ def ttt_bwd(q, k, v, lr, beta, w1, w2, w3, chunk, order, rule, dout, *, dw_out=N
     p = make_problem(q, k, w1, chunk, order, rule)
     errors = []
     opts, _keep = _options(p, update_mask, out_scale, m_in, q, allreduce, errors)
-    f32 = dict(device=q.device, dtype=torch.float32)
-    res = {"dq": torch.empty(q.shape, **f32), "dk": torch.empty(k.shape, **f32),
-           "dv": torch.empty(v.shape, **f32), "dlr": torch.empty(lr.shape, **f32),
-           "dbeta": None if beta is None else torch.empty(beta.shape, **f32),
-           "dw1": torch.empty(w1.shape, **f32), "dw2": torch.empty(w2.shape, **f32),
-           "dw3": torch.empty(w3.shape, **f32),
-           "dout_scale": None if out_scale is None else torch.empty(out_scale.shape, **f32)}
+
+    def f32(shape):
+        return _result(stream, torch.empty, shape, device=q.device, dtype=torch.float32)
+
+    res = {"dq": f32(q.shape), "dk": f32(k.shape), "dv": f32(v.shape), "dlr": f32(lr.shape),
+           "dbeta": None if beta is None else f32(beta.shape),
+           "dw1": f32(w1.shape), "dw2": f32(w2.shape), "dw3": f32(w3.shape),
+           "dout_scale": None if out_scale is None else f32(out_scale.shape)}
     need = _abi.bwd_workspace_bytes(p)
     if need == 0:
         raise LactError(_abi.LACT_EINVAL, "lact_ttt_bwd_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _made(stream, torch.empty, need, device=q.device, dtype=torch.uint8)
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     dw = (None, None, None) if dw_out is None else tuple(dw_out)
     mg = None
     if want_dm:
         B, H = q.shape[0], q.shape[1]
-        res["dm1"] = torch.empty((B * H, dh, d), **f32)
-        res["dm2"] = torch.empty((B * H, d, dh), **f32)
-        res["dm3"] = torch.empty((B * H, dh, d), **f32)
+        res["dm1"], res["dm2"], res["dm3"] = (f32((B * H, *s)) for s in ((dh, d), (d, dh), (dh, d)))
         dmo = (None, None, None) if dm_out is None else tuple(dm_out)
         mg = _abi.LactBwdMomentum(*(None if x is None else x.data_ptr()
                                     for x in dmo + (res["dm1"], res["dm2"], res["dm3"])))
@@ -352,9 +369,9 @@ def swa_fwd(q, k, v, q_scale, q_offset, k_scale, k_offset, window, *, out=None, 
     if need == 0:
         raise LactError(_abi.LACT_EINVAL, "lact_swa_workspace_bytes")
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     if workspace is None:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _made(stream, torch.empty, need, device=q.device, dtype=torch.uint8)
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     rc = _abi.lib().lact_swa_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(q_scale),

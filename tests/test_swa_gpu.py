@@ -97,3 +97,21 @@ def test_swa_with_wide_scales_and_offsets(d):
     err = rel_l2(got, want)
     assert err <= 2e-2, err
     print(f"swa wide scales d{d}: rel-L2 {err:.2e}")
+
+
+def test_own_stream_takes_no_block_in_use():
+    """A call on the current stream and, at once, one on another stream whose
+    inputs are there: the second does not take the first one's workspace
+    (d 512: the scores), which went back to the current stream's pool while
+    the first still runs."""
+    keys = ("q", "k", "v", "q_scale", "q_offset", "k_scale", "k_offset")
+    cases = [[make_swa_inputs(1, 2, 2048, 512, seed=s)[n].cuda() for n in keys] for s in (1, 2)]
+    alone = [ct.swa_fwd(*c, 512) for c in cases]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [ct.swa_fwd(*c, 512, stream=s) for c, s in zip(cases, (None, side))]
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            assert torch.equal(a, b)
+    assert ct.status() == ct.LACT_OK

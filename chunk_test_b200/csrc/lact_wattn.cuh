@@ -55,17 +55,35 @@ static bool injective(const View4& v, const Extent4& e) {
   return true;
 }
 
+// The bytes that a view covers within one period of `pitch` bytes: dimensions
+// that step by whole periods add nothing; -1 where one steps over part of one.
+static int64_t bytes_in_pitch(const View4& v, const Extent4& e, int64_t pitch, int esz) {
+  const int64_t s[3] = {v.sb, v.sh, v.st}, n[3] = {e.B, e.H, e.T};
+  int64_t w = e.d * esz;
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && s[i] * esz % pitch != 0) {
+      if (s[i] * esz > pitch) return -1;
+      w += (n[i] - 1) * s[i] * esz;
+    }
+  return w;
+}
+
 // Whether two views share no memory: their spans are apart, or both are slices
-// of one packed [B, T, row] buffer (equal row pitch) in different columns.
+// of one packed buffer, in different places of each of its rows, heads or
+// sequences: modulo the stride of one of the dimensions they do not meet.
 static bool apart(const View4& a, const Extent4& ea, const View4& b, const Extent4& eb, int esz) {
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
   if (!overlaps(a.p, static_cast<size_t>(span(a, ea)) * esz, b.p, static_cast<size_t>(span(b, eb)) * esz)) return true;
-  if (a.st != b.st || ea.T < 2 || eb.T < 2) return false;
-  if ((ea.B > 1 && a.sb % a.st != 0) || (eb.B > 1 && b.sb % b.st != 0)) return false;
-  const int64_t wa = (ea.H - 1) * a.sh + ea.d, wb = (eb.H - 1) * b.sh + eb.d;
-  const int64_t pitch = a.st * esz;
-  const int64_t at = static_cast<int64_t>(((static_cast<int64_t>(pb - pa)) % pitch + pitch) % pitch);
-  return at >= wa * esz && at + wb * esz <= pitch;
+  const int64_t strides[6] = {a.st, a.sh, a.sb, b.st, b.sh, b.sb}, n[6] = {ea.T, ea.H, ea.B, eb.T, eb.H, eb.B};
+  for (int i = 0; i < 6; ++i) {
+    if (n[i] < 2) continue;
+    const int64_t pitch = strides[i] * esz;
+    const int64_t wa = bytes_in_pitch(a, ea, pitch, esz), wb = bytes_in_pitch(b, eb, pitch, esz);
+    if (wa < 0 || wb < 0) continue;
+    const int64_t at = ((static_cast<int64_t>(pb - pa)) % pitch + pitch) % pitch;
+    if (at >= wa && at + wb <= pitch) return true;
+  }
+  return false;
 }
 static bool same(const View4& a, const View4& b, const Extent4& e) {
   return a.p == b.p && (e.B == 1 || a.sb == b.sb) && (e.H == 1 || a.sh == b.sh) && (e.T == 1 || a.st == b.st);

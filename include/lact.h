@@ -367,8 +367,9 @@ int lact_swa_fwd(const lact_swa_problem* p, const void* q, const void* k, const 
  * projection's [B, T, heads, d] result, or its slice of a packed one, is read
  * and written in place.  Data pointers are 16-byte aligned device pointers.
  * Outputs may not overlap themselves, one another or an input, except where
- * an entry point says so; two tensors with the same row pitch (stride_t) in
- * different columns of one packed buffer do not overlap. */
+ * an entry point says so; slices of one packed buffer that lie in different
+ * places of each of its rows, heads or sequences do not overlap, with one
+ * token or sequence too. */
 typedef struct lact_tensor4 {
   void* data;
   int64_t stride_b, stride_h, stride_t;

@@ -308,3 +308,63 @@ def test_own_stream_makes_its_tensors_there(monkeypatch):
         assert all(where == "side" for _, where in made), name
         got = [x for x in (kept.values() if isinstance(kept, dict) else kept if isinstance(kept, tuple) else [kept])]
         assert sorted(x.data_ptr() for x in got) == sorted(p for p, s in recorded if s == "main"), name
+
+
+def slices(B, T, heads, d, layout):
+    """The tensors of `heads` heads each that a packed buffer at G holds side by
+    side: in each row ("rows", [B, T, all heads, d]), in each sequence ("heads",
+    [B, all heads, T, d]) or in each head's row ("channels", [B, H, T, parts d])."""
+    n, total = len(heads), sum(heads)
+    at = [sum(heads[:i]) for i in range(n)]
+    if layout == "rows":
+        return [_abi.LactTensor4(G + 2 * a * d, T * total * d, d, total * d) for a in at]
+    if layout == "heads":
+        return [_abi.LactTensor4(G + 2 * a * T * d, total * T * d, T * d, d) for a in at]
+    return [_abi.LactTensor4(G + 2 * i * d, heads[0] * T * n * d, T * n * d, n * d) for i in range(n)]
+
+
+def rotary_bwd_rc(p, dq_out, dk_out, dq, dk):
+    """lact_rotary_bwd with too small a workspace: its layouts are looked at
+    before, so LACT_ENOSPC says that they are accepted.  Nothing is launched."""
+    far = lambda i, H: t4(i, p.B, H, p.T, p.d)  # noqa: E731
+    return ct.lib().lact_rotary_bwd(ref(p), ref(dq_out), ref(dk_out), 9 * G, None, ref(far(20, p.H)),
+                                    ref(far(21, p.Hkv)), 10 * G, 11 * G, ref(dq), ref(dk), 12 * G, 13 * G, 14 * G,
+                                    15 * G, 16 * G, ctypes.c_size_t(8), None)
+
+
+@pytest.mark.parametrize("layout", ["rows", "heads", "channels"])
+@pytest.mark.parametrize("B,T", [(1, 1), (2, 1), (8, 1), (1, 5), (2, 2), (8, 5)])
+def test_packed_slices_are_apart(B, T, layout):
+    """q and k of one packed buffer in place, one token per sequence too."""
+    heads = (4, 4, 4) if layout == "channels" else (4, 2, 2)
+    p = rot_problem(B=B, T=T, Hkv=heads[1])
+    q, k, v = slices(B, T, heads, 64, layout)
+    assert rotary_bwd_rc(p, q, k, q, k) == ct.LACT_ENOSPC
+    assert rotary_bwd_rc(p, k if layout == "channels" else q, v, q, k) == (
+        ct.LACT_EINVAL if layout == "channels" else ct.LACT_ENOSPC)
+    # one row of 16 bytes too far: into the neighbour
+    near = _abi.LactTensor4(k.data - 16, k.stride_b, k.stride_h, k.stride_t)
+    assert rotary_bwd_rc(p, q, near, q, near) == ct.LACT_EINVAL
+    # the attention's gradients beside one another
+    s = swa_problem(B=B, T=T, Tq=T, Hkv=heads[1])
+    far = lambda i, H: t4(i, B, H, T, 64)  # noqa: E731
+    for dv, want in ((v, ct.LACT_ENOSPC), (k, ct.LACT_EINVAL)):
+        rc = ct.lib().lact_swa_sink_bwd(ref(s), ref(far(20, 4)), ref(far(21, heads[1])), ref(far(22, heads[1])),
+                                        ref(far(23, 4)), 9 * G, ref(far(24, 4)), None, ref(q), ref(k), ref(dv), 10 * G,
+                                        ctypes.c_size_t(8), None)
+        assert rc == want
+
+
+def test_one_token_between_the_rows_of_another():
+    """A single row in the gap between another tensor's rows, and on one of them."""
+    p = rot_problem(B=1, H=1, Hkv=1, T=1)
+    row = t4(0, B=1, H=1, T=1)
+    for B, at, want in ((2, 64, ct.LACT_ENOSPC), (2, 128, ct.LACT_EINVAL), (2, 56, ct.LACT_EINVAL)):
+        s = swa_problem(B=B, H=1, Hkv=1, T=1, Tq=1)
+        far = lambda i: t4(i, B, 1, 1, 64)  # noqa: E731
+        dq = _abi.LactTensor4(G, 128, 64, 64)
+        dk = _abi.LactTensor4(G + 2 * at, 128, 64, 64)
+        rc = ct.lib().lact_swa_sink_bwd(ref(s), ref(far(20)), ref(far(21)), ref(far(22)), ref(far(23)), 9 * G, ref(far(24)),
+                                        None, ref(dq), ref(dk), ref(far(25)), 10 * G, ctypes.c_size_t(8), None)
+        assert rc == want, at
+    assert rotary_bwd_rc(p, row, t4(1, B=1, H=1, T=1), row, t4(0, B=1, H=1, T=1, at=16)) == ct.LACT_EINVAL

@@ -224,3 +224,32 @@ def test_refused_on_the_gpu():
         ct.rotary_fwd(q, k, freqs, start=-1)
     got = ct.rotary_fwd(q, k, freqs)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("layout", ["rows", "heads"])
+@pytest.mark.parametrize("B,T", [(1, 1), (5, 1), (3, 7)])
+def test_in_place_on_slices_of_one_buffer(B, T, layout):
+    """q and k of a packed [B, T, heads, d] or [B, heads, T, d] projection in
+    place, the step of one token per sequence among them, and the attention's
+    gradients written side by side."""
+    H, Hkv, d = 4, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(B + T)
+    shape = (B, T, H + 2 * Hkv, d) if layout == "rows" else (B, H + 2 * Hkv, T, d)
+    at = lambda x, i, n: x[:, :, i:i + n].transpose(1, 2) if layout == "rows" else x[:, i:i + n]  # noqa: E731
+    qkv = torch.randn(shape, generator=g, device="cuda").bfloat16()
+    kept = qkv.clone()
+    q, k, v = at(qkv, 0, H), at(qkv, H, Hkv), at(qkv, H + Hkv, Hkv)
+    freqs, _ = ct.rotary_frequencies(d)
+    want = ct.rotary_fwd(q, k, freqs, start=1000)
+    ct.rotary_fwd(q, k, freqs, start=1000, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(v, at(kept, H + Hkv, Hkv))
+    back = ct.rotary_bwd(q, k, freqs, start=1000)
+    out, lse = ct.swa_sink_fwd(q, k, v, 4, 1)
+    ref = ct.swa_sink_bwd(q, k, v, out, lse, out, 4, 1)
+    grads = torch.full_like(qkv, 7.0)
+    ct.swa_sink_bwd(q, k, v, out, lse, out, 4, 1, dq=at(grads, 0, H), dk=at(grads, H, Hkv), dv=at(grads, H + Hkv, Hkv))
+    for i, n, name in ((0, H, "dq"), (H, Hkv, "dk"), (H + Hkv, Hkv, "dv")):
+        assert torch.equal(at(grads, i, n), ref[name]), name
+    ct.rotary_bwd(q, k, freqs, start=1000, out=(q, k))
+    assert torch.equal(q, back["dq"]) and torch.equal(k, back["dk"])

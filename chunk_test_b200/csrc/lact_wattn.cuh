@@ -416,6 +416,8 @@ static int decode_validate(const lact_swa_sink_problem* p) {
   if (p->window < 1 || p->sinks < 0 || !std::isfinite(p->scale) || !(p->scale > 0.f))
     return LACT_EINVAL;
   if (p->window > (int64_t(1) << 30) || p->sinks > (int64_t(1) << 30)) return LACT_EINVAL;
+  // the kernels count slots in 32 bits, rounded up to whole steps of the cluster's CTAs
+  if (p->sinks + p->window > (int64_t(1) << 31) - 1024) return LACT_EINVAL;
   if (p->B * p->H > 65535) return LACT_EINVAL;
   return LACT_OK;
 }

@@ -473,7 +473,8 @@ int lact_swa_sink_bwd(const lact_swa_sink_problem* p, const lact_tensor4* q, con
  * every visible token, the new one included; out [B, H, 1, d].  `seen` is not
  * advanced.  A sequence with seen < 0 is inactive: out 0, cache untouched.
  * Slots that hold no token yet are not read.  One launch, no workspace.
- * Limits: d a multiple of 8 up to 256, B * H <= 65535, window, sinks <= 2^30. */
+ * Limits: d a multiple of 8 up to 256, B * H <= 65535, window, sinks <= 2^30,
+ * sinks + window <= 2^31 - 1024 (the same for lact_swa_cache_fill). */
 int lact_swa_sink_decode(const lact_swa_sink_problem* p, const lact_tensor4* q, const lact_tensor4* k,
                          const lact_tensor4* v, void* k_cache, void* v_cache, const int32_t* seen,
                          const lact_tensor4* out, void* stream);

@@ -368,3 +368,15 @@ def test_one_token_between_the_rows_of_another():
                                         None, ref(dq), ref(dk), ref(far(25)), 10 * G, ctypes.c_size_t(8), None)
         assert rc == want, at
     assert rotary_bwd_rc(p, row, t4(1, B=1, H=1, T=1), row, t4(0, B=1, H=1, T=1, at=16)) == ct.LACT_EINVAL
+
+
+@pytest.mark.parametrize("over", [1, 1024])
+def test_caches_past_the_kernels_32_bit_slots_refused(over):
+    """The last slots' numbers, rounded up, have to fit 32 bits; checked before anything is enqueued."""
+    window = (1 << 30) - 1024 + over
+    p = swa_problem(B=1, H=1, Hkv=1, T=1, Tq=1, d=8, window=window, sinks=1 << 30)
+    one = lambda i: t4(i, 1, 1, 1, 8)  # noqa: E731
+    lib, kc, vc = ct.lib(), 100 * G, 200 * G
+    assert lib.lact_swa_sink_decode(ref(p), ref(one(0)), ref(one(1)), ref(one(2)), kc, vc, 6 * G, ref(one(7)),
+                                    None) == ct.LACT_EINVAL
+    assert lib.lact_swa_cache_fill(ref(p), ref(one(0)), ref(one(1)), None, kc, vc, None) == ct.LACT_EINVAL

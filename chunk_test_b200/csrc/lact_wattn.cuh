@@ -19,6 +19,9 @@ struct Extent4 {
 // int32 and float32 arrays that are read singly (null: absent)
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// a * b <= 65535, for numbers of any size
+static bool product_ok(int64_t a, int64_t b) { return a <= 65535 && b <= 65535 && a * b <= 65535; }
+
 static bool view_ok(const lact_tensor4* t, const Extent4& e, int esz) {
   if (!t || !t->data || !aligned16(t->data)) return false;
   const int64_t s[3] = {t->stride_b, t->stride_h, t->stride_t}, n[3] = {e.B, e.H, e.T};
@@ -120,7 +123,8 @@ static int rotary_validate(const lact_rotary_problem* p) {
   if (!p || p->B < 1 || p->H < 1 || p->Hkv < 0 || p->T < 1 || p->d < 1) return LACT_EINVAL;
   if (p->dtype != LACT_F32 && p->dtype != LACT_BF16) return LACT_EINVAL;
   if (p->d % 8 != 0 || p->d > 512 || p->rot < 2 || p->rot > p->d || p->rot % 2 != 0) return LACT_EINVAL;
-  if (p->B * (p->H + p->Hkv) > 65535 || p->T > (int64_t(1) << 30) || p->B > 65535) return LACT_EINVAL;
+  if (!product_ok(p->B, p->H) || !product_ok(p->B, p->Hkv) || p->B * (p->H + p->Hkv) > 65535) return LACT_EINVAL;
+  if (p->T > (int64_t(1) << 30)) return LACT_EINVAL;
   if (p->start < 0 || p->start > (int64_t(1) << 40) || (p->interleaved & ~1)) return LACT_EINVAL;
   if (!(std::isfinite(p->amplitude))) return LACT_EINVAL;
   return LACT_OK;
@@ -206,7 +210,7 @@ static int wattn_validate(const lact_swa_sink_problem* p, WattnDims& D) {
   if (p->H % p->Hkv != 0 || p->Tq > p->T || p->d % 8 != 0 || p->d > 256) return LACT_EINVAL;
   if (p->window < 1 || p->sinks < 0 || !std::isfinite(p->scale) || !(p->scale > 0.f))
     return LACT_EINVAL;
-  if (p->B * p->H > 65535 || p->T > (int64_t(1) << 24)) return LACT_EINVAL;
+  if (!product_ok(p->B, p->H) || p->T > (int64_t(1) << 24)) return LACT_EINVAL;
   D.B = p->B; D.H = p->H; D.Hkv = p->Hkv; D.T = p->T; D.Tq = p->Tq; D.d = p->d;
   D.DP = rup(p->d, 64);
   D.window = static_cast<int>(std::min(p->window, p->T));
@@ -418,7 +422,7 @@ static int decode_validate(const lact_swa_sink_problem* p) {
   if (p->window > (int64_t(1) << 30) || p->sinks > (int64_t(1) << 30)) return LACT_EINVAL;
   // the kernels count slots in 32 bits, rounded up to whole steps of the cluster's CTAs
   if (p->sinks + p->window > (int64_t(1) << 31) - 1024) return LACT_EINVAL;
-  if (p->B * p->H > 65535) return LACT_EINVAL;
+  if (!product_ok(p->B, p->H)) return LACT_EINVAL;
   return LACT_OK;
 }
 

@@ -380,3 +380,22 @@ def test_caches_past_the_kernels_32_bit_slots_refused(over):
     assert lib.lact_swa_sink_decode(ref(p), ref(one(0)), ref(one(1)), ref(one(2)), kc, vc, 6 * G, ref(one(7)),
                                     None) == ct.LACT_EINVAL
     assert lib.lact_swa_cache_fill(ref(p), ref(one(0)), ref(one(1)), None, kc, vc, None) == ct.LACT_EINVAL
+
+
+@pytest.mark.parametrize("sizes", [dict(B=1 << 32, H=1 << 32, Hkv=1 << 32), dict(B=1 << 62, H=4, Hkv=4),
+                                   dict(B=4, H=1 << 62, Hkv=1 << 62), dict(B=2, H=1 << 62, Hkv=1 << 62)])
+def test_products_past_64_bits_refused(sizes):
+    """Batches times heads of 2^63 and more, whose product wraps to a small number."""
+    lib = ct.lib()
+    for T in (1, 64):
+        p, r = swa_problem(T=T, Tq=T, **sizes), rot_problem(T=T, **sizes)
+        assert lib.lact_swa_sink_bwd_workspace_bytes(ref(p)) == 0
+        assert lib.lact_rotary_bwd_workspace_bytes(ref(r)) == 0
+        t = lambda i: t4(i, 2, 1, T)  # noqa: E731
+        assert lib.lact_swa_sink_fwd(ref(p), ref(t(0)), ref(t(1)), ref(t(2)), None, ref(t(3)), 9 * G, None) == ct.LACT_EINVAL
+        assert lib.lact_rotary_fwd(ref(r), ref(t(0)), ref(t(1)), 9 * G, *[None] * 5, ref(t(2)), ref(t(3)), None) == ct.LACT_EINVAL
+    p = swa_problem(T=1, Tq=1, **sizes)
+    t = lambda i: t4(i, 2, 1, 1)  # noqa: E731
+    assert lib.lact_swa_sink_decode(ref(p), ref(t(0)), ref(t(1)), ref(t(2)), 4 * G, 5 * G, 6 * G, ref(t(7)),
+                                    None) == ct.LACT_EINVAL
+    assert lib.lact_swa_cache_fill(ref(p), ref(t(0)), ref(t(1)), None, 4 * G, 5 * G, None) == ct.LACT_EINVAL

@@ -682,7 +682,10 @@ int lact_swa_sink_decode(const lact_swa_sink_problem* p, const lact_tensor4* q, 
 int lact_swa_cache_fill(const lact_swa_sink_problem* p, const lact_tensor4* k, const lact_tensor4* v,
                         const int32_t* lengths, void* k_cache, void* v_cache, void* stream) {
   using namespace lact;
-  const int rc = decode_validate(p);
+  if (!p) return LACT_EINVAL;
+  lact_swa_sink_problem keys = *p;   // there are no queries
+  keys.H = p->Hkv;
+  const int rc = decode_validate(&keys);
   if (rc != LACT_OK) return rc;
   if (p->T < 1 || p->T > (int64_t(1) << 24)) return LACT_EINVAL;
   const int esz = p->dtype == LACT_BF16 ? 2 : 4;

@@ -399,3 +399,23 @@ def test_products_past_64_bits_refused(sizes):
     assert lib.lact_swa_sink_decode(ref(p), ref(t(0)), ref(t(1)), ref(t(2)), 4 * G, 5 * G, 6 * G, ref(t(7)),
                                     None) == ct.LACT_EINVAL
     assert lib.lact_swa_cache_fill(ref(p), ref(t(0)), ref(t(1)), None, 4 * G, 5 * G, None) == ct.LACT_EINVAL
+
+
+def test_cache_fill_has_no_use_for_queries():
+    """H and Tq may hold anything.  The last check before the launch, the caches'
+    overlap, cannot tell (it gives LACT_EINVAL too), so the call is made from a
+    child whose device is hidden: past the checks it finds none."""
+    import os
+    import subprocess
+    import sys
+    code = ("import ctypes, chunk_test_b200 as ct\n"
+            "from tests.test_attention_host import swa_problem, t4, G, ref\n"
+            "for H, Tq in ((0, 64), (3, 64), (-1, 0), (1 << 40, 1 << 40)):\n"
+            "    p = swa_problem(H=H, Tq=Tq)\n"
+            "    rc = ct.lib().lact_swa_cache_fill(ref(p), ref(t4(0, H=2)), ref(t4(1, H=2)), None, 4 * G, 5 * G, None)\n"
+            "    assert rc == -3, (H, Tq, rc)\n"
+            "assert ct.lib().lact_swa_cache_fill(None, None, None, None, None, None, None) == -1\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         env={**os.environ, "CUDA_VISIBLE_DEVICES": "", "PYTHONPATH": root})
+    assert run.returncode == 0, run.stderr

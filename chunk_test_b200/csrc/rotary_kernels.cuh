@@ -30,6 +30,9 @@ struct View4 {
 
 constexpr int kRotaryThreads = 384;    // of a block, 512 where a thread owns single channels
 constexpr int kRotaryTile = 16;        // tokens whose angles are held at a time
+// upper half of the turn that marks the pairs which pad a row's last vector: a NaN
+// of its own, so that a frequency that is not a number is still one
+constexpr int kPadTurn = 0x7ff85ad0;
 
 struct RotaryParams {
   View4 xq, xk;            // forward: inputs; backward: inputs, for the scales' gradients (else null)
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : kRotaryThreads, V == 1 ? 1 : 2)
   double* turns = reinterpret_cast<double*>(trig + kRotaryTile * row_pairs);
   for (int x = threadIdx.x; x < row_pairs; x += blockDim.x) {
     const int i = (x % p.rot_units) * kPairs + x / p.rot_units;
-    turns[x] = 2 * i < p.rot ? p.freqs[i] * 0.15915494309189533577 : nan("");   // 1 / (2 pi); a pad passes through
+    turns[x] = 2 * i < p.rot ? p.freqs[i] * 0.15915494309189533577 : __hiloint2double(kPadTurn, 0);   // 1 / (2 pi)
   }
   const int step_t = blockDim.x / row_pairs, step_x = blockDim.x % row_pairs;
   const int first_t = threadIdx.x / row_pairs, first_x = threadIdx.x % row_pairs;
@@ -193,10 +196,10 @@ __global__ void __launch_bounds__(V == 1 ? 512 : kRotaryThreads, V == 1 ? 1 : 2)
     for (int t = first_t, x = first_x; t < nt;) {
       const int64_t tok = t0 + base + t;
       const int64_t pos = p.positions ? p.positions[b * p.T + tok] : p.start + tok;
-      const double n = static_cast<double>(pos) * turns[x];
+      const double turn = turns[x], n = static_cast<double>(pos) * turn;
       float s, c;
       sincospif(static_cast<float>(2.0 * (n - rint(n))), &s, &c);
-      const bool pad = INTER && isnan(n);
+      const bool pad = INTER && __double2hiint(turn) == kPadTurn;   // passes through
       trig[t * row_pairs + x] = make_float2(pad ? 1.f : p.amp * c, pad ? 0.f : p.amp * (BWD ? -s : s));
       t += step_t;
       x += step_x;

@@ -253,3 +253,21 @@ def test_in_place_on_slices_of_one_buffer(B, T, layout):
         assert torch.equal(at(grads, i, n), ref[name]), name
     ct.rotary_bwd(q, k, freqs, start=1000, out=(q, k))
     assert torch.equal(q, back["dq"]) and torch.equal(k, back["dk"])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot,bad", [(16, float("nan")), (16, float("inf")), (6, float("nan")), (6, -float("inf"))])
+def test_a_frequency_that_is_no_number_shows(rot, bad, inter):
+    """Its pair is NaN at every position, in both layouts; the other channels are
+    what they are without."""
+    q, k, _ = inputs(2, 2, 1, 20, 32, torch.bfloat16)
+    freqs, _ = ct.rotary_frequencies(rot)
+    want = ct.rotary_fwd(q, k, freqs, interleaved=inter)
+    back = ct.rotary_bwd(q, k, freqs, interleaved=inter)
+    freqs[1] = bad
+    pair = [2, 3] if inter else [1, 1 + rot // 2]
+    rest = [c for c in range(32) if c not in pair]
+    got, gb = ct.rotary_fwd(q, k, freqs, interleaved=inter), ct.rotary_bwd(q, k, freqs, interleaved=inter)
+    for a, b in ((got[0], want[0]), (got[1], want[1]), (gb["dq"], back["dq"]), (gb["dk"], back["dk"])):
+        assert bool(torch.isnan(a[..., pair]).all())
+        assert torch.equal(a[..., rest], b[..., rest])

@@ -69,6 +69,7 @@ static int validate(const lact_problem* p, Dims& D) {
   if (!p) return LACT_EINVAL;
   if (p->B < 1 || p->H < 1 || p->T < 1 || p->Tq < 1 || p->d < 1 || p->dh < 1 || p->chunk < 1)
     return LACT_EINVAL;
+  if (p->B > 4096 || p->H > 4096) return LACT_EINVAL;   // before their product, which is limited below
   if (p->order != LACT_APPLY_THEN_UPDATE && p->order != LACT_UPDATE_THEN_APPLY) return LACT_EINVAL;
   if (p->rule < LACT_RULE_GD || p->rule > LACT_RULE_MUON) return LACT_EINVAL;
   if (p->dtype != LACT_F32 && p->dtype != LACT_BF16) return LACT_EINVAL;

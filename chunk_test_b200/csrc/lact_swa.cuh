@@ -32,7 +32,7 @@ static int swa_validate(const lact_swa_problem* p, SwaDims& S) {
   if (p->B < 1 || p->H < 1 || p->T < 1 || p->d < 1 || p->window < 1) return LACT_EINVAL;
   if (p->dtype != LACT_BF16) return LACT_EINVAL;
   if (p->d % 64 != 0 || p->d > 512 || p->T % 128 != 0 || p->window % 128 != 0) return LACT_EINVAL;
-  if (p->B * p->H > 4096 || p->T > (int64_t(1) << 24) || p->window > 16384) return LACT_EINVAL;
+  if (p->B > 4096 || p->H > 4096 || p->B * p->H > 4096 || p->T > (int64_t(1) << 24) || p->window > 16384) return LACT_EINVAL;
   S.B = p->B; S.H = p->H; S.BH = p->B * p->H; S.T = p->T; S.d = p->d; S.window = p->window;
   S.nb = S.T / 128;
   S.nbp = (S.window + S.T) / 128;

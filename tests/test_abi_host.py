@@ -242,3 +242,14 @@ def test_attention_workspace_follows_the_documented_layout():
     padded = 2 * (B * H * (w + T) + w) * d * 2
     assert got >= B * H * T * d * 2 + scores + padded
     assert got <= B * H * T * d * 2 + scores + padded + 4 * 256
+
+
+@pytest.mark.parametrize("B,H", [(1 << 32, 1 << 32), (1 << 62, 4), (4, 1 << 62)])
+def test_products_past_64_bits_refused(B, H):
+    """Batches times heads whose product wraps to zero."""
+    lib, w = ct.lib(), WORKLOADS[1]
+    p = ctypes.byref(_prob(w, B=B, H=H))
+    assert lib.lact_ttt_workspace_bytes(p) == 0
+    assert lib.lact_ttt_bwd_workspace_bytes(p) == 0
+    assert lib.lact_ttt_host_workspace_bytes(p) == 0
+    assert lib.lact_swa_workspace_bytes(ctypes.byref(_abi.LactSwaProblem(B, H, 256, 64, 128, _abi.LACT_BF16, 0))) == 0

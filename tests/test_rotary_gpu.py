@@ -271,3 +271,35 @@ def test_a_frequency_that_is_no_number_shows(rot, bad, inter):
     for a, b in ((got[0], want[0]), (got[1], want[1]), (gb["dq"], back["dq"]), (gb["dk"], back["dk"])):
         assert bool(torch.isnan(a[..., pair]).all())
         assert torch.equal(a[..., rest], b[..., rest])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,Hkv,T,d,rot,inter", [
+    (13, 3, 37, 256, 256, False),      # 12 heads a block: whole vectors, two blocks of heads
+    (40, 8, 21, 128, 64, False),       # pairs and passing channels in one block of several heads
+    (30, 5, 33, 96, 50, False),        # single channels: 5 heads a block
+    (33, 8, 19, 128, 128, True),
+    (1, 1, 700, 8, 8, False),          # one unit a head
+])
+def test_more_heads_than_a_block_holds(H, Hkv, T, d, rot, inter, dtype):
+    q, k, g = inputs(2, H, Hkv, T, d, dtype, "bthd", seed=T)
+    dq, dk, _ = inputs(2, H, Hkv, T, d, dtype, seed=T + 1)
+    freqs, _ = ct.rotary_frequencies(rot)
+    pos = torch.arange(T, device="cuda").expand(2, T)
+    kw = params(H, Hkv, d, g)
+    got = ct.rotary_fwd(q, k, freqs, interleaved=inter, **kw)
+    res = ct.rotary_bwd(dq, dk, freqs, interleaved=inter, q=q, k=k, **kw)
+    plain = ct.rotary_bwd(dq, dk, freqs, interleaved=inter)
+    for x, y, dy, n in ((q, got[0], dq, "q"), (k, got[1], dk, "k")):
+        sc, of = kw[n + "_scale"], kw[n + "_offset"]
+        size = (x.double() * sc.double()[:, None]).abs() + of.double().abs()[:, None]
+        check(y, ao.rotary(x, freqs, pos, inter, 1.0, sc, of), partner_sum(size, rot, inter), 1.0)
+        dx, ds, do, ads, ado = ao.rotary_vjp(dy, freqs, pos, inter, 1.0, x, sc)
+        pair = partner_sum(dy.double(), rot, inter)
+        check(res["d" + n], dx, pair * sc.double().abs()[:, None], 1.0)
+        check(plain["d" + n], ao.rotary_vjp(dy, freqs, pos, inter)[0], pair, 1.0)
+        t = 400 * 2.0 ** -24 + 2.0 ** -20
+        slack = 2.0 ** -20 * (pair * x.double().abs()).sum((0, 2)), 2.0 ** -20 * pair.sum((0, 2))
+        assert bool(((res[f"d{n}_scale"].double() - ds).abs() <= t * ads + slack[0]).all())
+        assert bool(((res[f"d{n}_offset"].double() - do).abs() <= t * ado + slack[1]).all())
+    assert ct.status() == ct.LACT_OK

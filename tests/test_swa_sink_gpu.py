@@ -387,3 +387,36 @@ def test_own_stream_takes_no_block_in_use():
         for a, b in zip(got, alone):
             for n in a:
                 assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,H,Hkv,T,Tq,d,window,sinks,lengths,layout", [
+    (2, 2, 1, 900, 900, 256, 256, 4, None, "bhtd"),             # the language model's head dim with sinks
+    (2, 3, 3, 1500, 1500, 256, 200, 4, (1500, 1130), "bthd"),   # far parts, a length inside a half tile of values
+    (4, 4, 2, 400, 400, 256, 100, 4, (400, 0, 193, 63), "bhtd"),
+    (2, 2, 1, 700, 333, 256, 130, 8, (700, 650), "bthd"),       # the last 333 positions
+    (1, 2, 2, 600, 1, 256, 70, 5, None, "bhtd"),
+    (3, 2, 1, 500, 500, 192, 129, 16, (500, 320, 1), "bthd"),
+    (2, 2, 2, 513, 200, 192, 130, 5, (513, 449), "bhtd"),
+    (3, 4, 1, 700, 700, 128, 100, 16, (700, 450, 64), "bthd"),
+    (2, 4, 2, 640, 257, 128, 64, 130, (640, 511), "bhtd"),
+    (1, 2, 1, 1100, 1100, 256, 100, 260, (1037,), "bthd"),      # sinks over three tiles
+    (2, 1, 1, 300, 300, 200, 64, 3, (300, 129), "bhtd"),        # a padded head dim above 192
+])
+def test_lengths_sinks_and_late_queries_at_each_head_dim(B, H, Hkv, T, Tq, d, window, sinks, lengths, layout, dtype):
+    """Above d 128 the values come in half tiles and the last product's operand is
+    refilled by halves: with sinks, lengths and Tq < T, NaN behind the lengths."""
+    q, k, v, dout = make(B, H, Hkv, T, Tq, d, dtype, layout, seed=T + d)
+    lens = None
+    if lengths is not None:
+        lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        for b, n in enumerate(lengths):
+            q[b, :, max(n - (T - Tq), 0):] = math.nan
+            dout[b, :, max(n - (T - Tq), 0):] = math.nan
+            k[b, :, n:], v[b, :, n:] = math.nan, math.inf
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lens)
+    w = ao.attention(q, k, v, window, sinks, lengths, dout=dout)
+    check_forward(out, lse, w, dtype, d, min(T, window + sinks))
+    res = ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks, lengths=lens)
+    check_backward(res, w, dtype, d, T * (H // Hkv))
+    assert ct.status() == ct.LACT_OK

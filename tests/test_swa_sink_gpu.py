@@ -420,3 +420,23 @@ def test_lengths_sinks_and_late_queries_at_each_head_dim(B, H, Hkv, T, Tq, d, wi
     res = ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks, lengths=lens)
     check_backward(res, w, dtype, d, T * (H // Hkv))
     assert ct.status() == ct.LACT_OK
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("B,H,T", [(8, 8, 1000), (9, 8, 1000), (3, 24, 2600), (8, 2, 300), (40, 6, 700)])
+def test_a_ragged_batch_is_its_sequences(B, H, T, d):
+    """On both sides of the rules for the order of the tiles: each sequence of a
+    ragged batch gets the same bits as alone."""
+    window, sinks = 150, 4
+    lengths = [(T if b == 1 else (613 * b + 7) % T) for b in range(B)]
+    q, k, v, dout = make(B, H, 2, T, T, d, BF16, "bthd", seed=B)
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = ct.swa_sink_fwd(q, k, v, window, sinks, lengths=lens)
+    res = ct.swa_sink_bwd(q, k, v, out, lse, dout, window, sinks, lengths=lens)
+    for b in range(B):
+        x = [t[b:b + 1] for t in (q, k, v)]
+        o, l = ct.swa_sink_fwd(*x, window, sinks, lengths=lens[b:b + 1])
+        assert torch.equal(out[b:b + 1], o) and torch.equal(lse[b:b + 1], l), b
+        g = ct.swa_sink_bwd(*x, o, l, dout[b:b + 1], window, sinks, lengths=lens[b:b + 1])
+        assert torch.equal(res["dq"][b:b + 1], g["dq"]), b   # the sinks' far parts follow the batch
+    assert ct.status() == ct.LACT_OK

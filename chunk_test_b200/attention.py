@@ -11,6 +11,7 @@ then make their results and workspaces).
 """
 from __future__ import annotations
 
+import functools
 import math
 import struct
 
@@ -40,6 +41,8 @@ def _view(t):
 
 def _new(t, stream):
     """A new contiguous result like `t`."""
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     return _result(stream, torch.empty_like, t, memory_format=torch.contiguous_format)
 
 
@@ -208,10 +211,11 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
         if q is None or (dk_out is not None and k is None):
             raise ValueError("the scales' gradients need the forward's q and k")
         _tensor("q", q, dq_out.shape, dq_out)
-        res["dq_scale"], res["dq_offset"] = _new(q_scale, stream), _new(q_scale, stream)
+        like = torch.empty_like if stream is None else functools.partial(_result, stream, torch.empty_like)
+        res["dq_scale"], res["dq_offset"] = like(q_scale), like(q_scale)
         if dk_out is not None:
             _tensor("k", k, dk_out.shape, dq_out)
-            res["dk_scale"], res["dk_offset"] = _new(k_scale, stream), _new(k_scale, stream)
+            res["dk_scale"], res["dk_offset"] = like(k_scale), like(k_scale)
         need = int(_abi.lib().lact_rotary_bwd_workspace_bytes(p))
         if need == 0:
             raise LactError(_abi.LACT_EINVAL, "lact_rotary_bwd_workspace_bytes")
@@ -225,6 +229,8 @@ def rotary_bwd(dq_out, dk_out, freqs, *, positions=None, start=0, interleaved=Fa
 
 def _workspace(workspace, need, device, stream):
     if workspace is None:
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=device)
         return _made(stream, torch.empty, need, dtype=torch.uint8, device=device)
     if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the device of the call")
@@ -263,7 +269,8 @@ def swa_sink_fwd(q, k, v, window, sinks=0, *, lengths=None, scale=None, out=None
     else:
         _tensor("out", out, q.shape, q)
     if lse is None:
-        lse = _result(stream, torch.empty, q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32) if stream is None else _result(
+            stream, torch.empty, q.shape[:3], dtype=torch.float32, device=q.device)
     else:
         _dense("lse", lse, q.shape[:3], torch.float32, q.device)
     _call("lact_swa_sink_fwd", q.device, stream, p, _view(q), _view(k), _view(v), _at(lengths), _view(out), _at(lse))

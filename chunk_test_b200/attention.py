@@ -340,7 +340,9 @@ def swa_sink_decode(q, k, v, k_cache, v_cache, seen, window, sinks=0, *, scale=N
 def swa_cache_fill(k, v, k_cache, v_cache, window, sinks=0, *, lengths=None, stream=None):
     """A prompt's k, v [B, Hkv, T, d] into the rolling caches of
     swa_sink_decode (lact_swa_cache_fill): the sinks and the last `window`
-    other tokens of each sequence; `seen` is then the sequences' lengths."""
+    other tokens of each sequence; `seen` is then the sequences' lengths.
+    The tokens are those from position 0 on: a prompt in pieces is filled in
+    after its last piece."""
     _query(k)
     B, Hkv, T, d = k.shape
     p = _swa_sink_problem(k, k, window, sinks, 1.0, T, 1)

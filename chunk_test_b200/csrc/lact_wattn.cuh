@@ -433,8 +433,11 @@ static int decode_validate(const lact_swa_sink_problem* p) {
 
 // CTAs of one (sequence, key head): doubled while the whole grid would leave
 // SMs idle and each CTA keeps 16 slots for each of its warps.  More CTAs than
-// that cost more in joining than they balance (64 sequences, 4 key heads, d 128,
-// windows of 8192: 189 us with one, 257 us with four).  16 is the largest cluster.
+// that cost more in joining full windows than they balance (4 key heads, d 128,
+// windows of 8192: 64 full sequences 184 us with one, 190 with two, 201 with four;
+// at lengths from none to the whole window 162, 157 and 154; 32 full ones 101 with
+// two, 105 with four; 8 full ones 37 with eight, 55 with sixteen).  16 is the
+// largest cluster.
 static int decode_ranks(int64_t items, int64_t slots) {
   int r = 1;
   while (r < 16 && items * r < kPlanSMs && slots >= static_cast<int64_t>(r) * 2 * kDecWarps * 16) r *= 2;

@@ -28,8 +28,8 @@
 // passes of 9 tiles repeat; at d = 256 by the chain S, dS, dX of one tile (about
 // 5400 clocks for 3 x 1024 of products), for TMEM holds one S beside 256 columns of
 // dX, and shared memory one B1.  Measured: B 2, H 6, T 8192, d 256, window 2048,
-// 4 sinks: dQ 306 us, dK and dV 554; B 2, 12 heads on 4, T 4001, d 128, window
-// 1000, 8 sinks: 103 and 173.
+// 4 sinks: dQ 325 us, dK and dV 580 in a row of calls; B 2, 12 heads on 4, T 4001,
+// d 128, window 1000, 8 sinks: 102 and 175.
 #pragma once
 
 #include "wattn_fwd.cuh"

@@ -34,12 +34,15 @@ __device__ __forceinline__ int seq_len(const WattnParams& p, int b) {
 // The v-th query tile of 128 rows in the order in which persistent CTAs take
 // them.  by_length (the forward of a few sequences, for their lengths are walked):
 // first the tiles that hold tokens, then the tiles behind the lengths, which are
-// only filled; else sequence after sequence.  (dQ gains nothing by it: 90 ragged
-// batches took 0 to 7% longer.)  The later positions of a sequence first (the first
+// only filled; else sequence after sequence.  (dQ gains nothing by it: over 90 ragged
+// batches the backward took 1% less to 7% more, by the number of sequences.)  The
+// later positions of a sequence first (the first
 // window's tiles see fewer keys).  heads_first: all heads of a sequence at one
-// position together, so that its short tiles are its last: for few rounds (the
-// dQ of 768 tiles on 148 SMs: 324 us, 362 head by head).  Else head by head, whose
-// CTAs share keys in L2 (the forward of 24 times 128 tiles: 718 us, 752 the other way).
+// position together, so that its short tiles are its last: for few rounds (B 2, H 6,
+// T 8192, d 256, window 2048: the backward 933 us, 983 head by head; the forward
+// 194, 204).  Else head by head, whose CTAs share keys in L2 (H 64, T 16384, d 128,
+// window 4096: the backward 8674 us, 9045 the other way; the forward gains nothing
+// by it: 844 and 839 at B 2, H 6, T 32768, d 256).
 struct TileAt {
   int b, h, m;
 };

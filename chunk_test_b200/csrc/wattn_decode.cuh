@@ -9,13 +9,14 @@
 // cache; its key and value come from the call's k and v, so the CTA that
 // writes the slot races with nobody.
 //
-// Bound by HBM (each key and value is read once for all of the group's heads)
-// and, for few sequences, by latency: the slots of one (sequence, key head)
+// Bound by HBM (each key and value is read once for up to 8 of the group's heads,
+// again for each 8 more) and, for few sequences, by latency: the slots of one (sequence, key head)
 // are split over a thread-block cluster, whose CTAs join their softmax
 // statistics and sums through distributed shared memory in rank order -- one
 // launch, no workspace, no atomics, the same bits on every run.  Measured: 64
-// sequences of 0 to 16512 tokens, 12 heads on 4, d 128, window 8192: 151 us, 5.3
-// TB/s; one sequence, 6 heads, d 256, window 2048: about 10 us of which 2 are bytes.
+// sequences of 0 to 16512 tokens, 12 heads on 4, d 128, window 8192: 157 us, 5.1
+// TB/s; one sequence, 6 heads, d 256, window 2048: 8.7 us in a graph of such calls,
+// of which 2 are bytes.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kDecThreads, DP <= 128 ? 2 : 1) k_wattn_decode
 #pragma unroll
       for (int i = 0; i < 2; ++i) e[nb][i] = ex2_approx(sc[nb][i] - base);
     l = l * fix + ((e[0][0] + e[0][1]) + (e[1][0] + e[1][1]));
-    // the products' probabilities in bf16 (half a step, 2^-9 of each); the sum keeps 32 bits
+    // the products' probabilities in bf16 (half a step, 2^-8 of each); the sum keeps 32 bits
     const uint32_t p0 = pack_bf16x2(e[0][0], e[0][1]), p1 = pack_bf16x2(e[1][0], e[1][1]);
     if (__any_sync(0xffffffffu, fix != 1.f)) {
       const float f0 = __shfl_sync(0xffffffffu, fix, 8 * t), f1 = __shfl_sync(0xffffffffu, fix, 8 * t + 4);

@@ -22,7 +22,8 @@
 //
 // Bound, above d = 128, by the tensor pipe and what the issuing thread waits:
 // about 3000 clocks a tile for 2048 of products at d = 256 (B 2, H 6, T 32768,
-// window 2048, 4 sinks: 718 us, 1115 TFLOP/s).  Up to d = 128 by the latency of
+// window 2048, 4 sinks: 862 us in a row of calls, 929 TFLOP/s, where the 1000 W
+// cap holds the clock down; 766 us after a pause).  Up to d = 128 by the latency of
 // S, softmax and P V in turn: 2900 clocks a tile and SM for 1024 of products and
 // as many of exponentials at 16 per clock (B 3 of up to 5000 tokens, 12 heads on
 // 4, d 128, window 1000: 107 us).

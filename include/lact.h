@@ -481,7 +481,10 @@ int lact_swa_sink_decode(const lact_swa_sink_problem* p, const lact_tensor4* q, 
 
 /* A prompt's k, v [B, Hkv, T, d] (T <= 2^24, lengths as above) into the
  * caches: the sinks and the last `window` other tokens of each sequence, each
- * in its slot; other slots keep what they hold.  H and Tq are not used. */
+ * in its slot; other slots keep what they hold.  Positions start at 0: where a
+ * prompt is attended to in pieces (Tq < T), its keys and values are kept until
+ * the last piece and filled in together; a cache that holds tokens is continued
+ * by lact_swa_sink_decode alone, one token a call.  H and Tq are not used. */
 int lact_swa_cache_fill(const lact_swa_sink_problem* p, const lact_tensor4* k, const lact_tensor4* v,
                         const int32_t* lengths, void* k_cache, void* v_cache, void* stream);
 

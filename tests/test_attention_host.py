@@ -419,3 +419,50 @@ def test_cache_fill_has_no_use_for_queries():
     run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
                          env={**os.environ, "CUDA_VISIBLE_DEVICES": "", "PYTHONPATH": root})
     assert run.returncode == 0, run.stderr
+
+
+def test_accepted_layouts_share_no_address():
+    """Random strides and offsets of dq and dk in one small buffer: what is
+    accepted (LACT_ENOSPC, see rotary_bwd_rc) shares no element, and nothing is
+    written twice."""
+    import itertools
+    import random
+    rng = random.Random(0)
+    far = {}
+    seen = {ct.LACT_ENOSPC: 0, ct.LACT_EINVAL: 0}
+    packed = 0
+
+    def elements(at, strides, n):
+        return [at + sum(i * s for i, s in zip(ix, strides)) + c
+                for ix in itertools.product(*(range(x) for x in n)) for c in range(8)]
+
+    for _ in range(4000):
+        B, Hkv, T = (rng.choice([1, 2, 3]) for _ in range(3))
+        H = Hkv * rng.choice([1, 2])
+        p = swa_problem(B=B, H=H, Hkv=Hkv, T=T, Tq=T, d=8)
+        key = (B, H, Hkv, T)
+        if key not in far:
+            far[key] = [t4(20 + i, B, h, T, 8) for i, h in enumerate((H, Hkv, Hkv, H, H, Hkv))]
+        x = far[key]
+        if rng.random() < 0.5:    # nested in some order, with gaps
+            row, order = 8, rng.sample(range(3), 3)
+            one = [0, 0, 0]
+            for i in order:
+                row *= rng.choice([1, 2, 3])
+                one[i] = row
+                row *= (B, H, T)[i]
+            other = list(one) if rng.random() < 0.7 else [8 * rng.randint(1, 30) for _ in range(3)]
+        else:
+            one, other = ([8 * rng.randint(1, 30) for _ in range(3)] for _ in range(2))
+        at = 8 * rng.randint(0, 40)
+        dq, dk = _abi.LactTensor4(G, *one), _abi.LactTensor4(G + 2 * at, *other)
+        rc = ct.lib().lact_swa_sink_bwd(ref(p), ref(x[0]), ref(x[1]), ref(x[2]), ref(x[3]), 9 * G, ref(x[4]), None,
+                                        ref(dq), ref(dk), ref(x[5]), 10 * G, ctypes.c_size_t(8), None)
+        seen[rc] += 1
+        if rc != ct.LACT_ENOSPC:
+            continue
+        a, b = elements(0, one, (B, H, T)), elements(at, other, (B, Hkv, T))
+        assert len(set(a)) == len(a) and len(set(b)) == len(b), (key, one, other)
+        assert not set(a) & set(b), (key, one, other, at)
+        packed += max(a) > min(b) and max(b) > min(a)
+    assert packed > 100 and min(seen.values()) > 500, (packed, seen)
